@@ -358,6 +358,115 @@ mcs_status mcs_sparse_step_blocks(const void *Q, const void *K, const void *V, i
                                   const int32_t *pair_len, const float *residual, float scale, void *O,
                                   mcs_stream_t stream);
 
+/*
+ * Rotary positions and a cache of earlier tokens -- what a model that
+ * generates chunk by chunk needs around the entry points above: queries and
+ * keys rotated by their positions, the keys and values of finished tokens kept
+ * in 8 bits, and attention from each new chunk to everything kept.
+ */
+
+typedef enum { MCS_BF16 = 0, MCS_FP16 = 1, MCS_FP32 = 2 } mcs_dtype;
+
+/* The pairs of a head that turn with the position, and how fast.  Pair i is
+ * the numbers (i, pairs + i) of the head, or (2i, 2i + 1) when interleaved;
+ * numbers from 2 * pairs on stay.  It turns by position[axis[i]] times
+ * turns[i] / 2^64 of a full turn (turns = round(f / 2pi * 2^64) for f radians
+ * per position: exact mod whole turns at every 32-bit position).  axes: numbers
+ * per position; every axis[i] in [0, axes).  magnitude: factor on the rotated
+ * numbers, > 0.  Both arrays in device memory. */
+typedef struct {
+  const uint64_t *turns; /* [pairs] */
+  const int32_t *axis;   /* [pairs] */
+  int32_t pairs, interleaved, axes;
+  float magnitude;
+} mcs_rotary;
+
+/*
+ * mcs_rotate -- out = x with each head's pairs turned by the token's position:
+ *   a' = magnitude (a cos t - b sin t),  b' = magnitude (a sin t + b cos t);
+ * with back != 0 by -t (times magnitude): the gradient of the forward map.
+ * x: [B, H, N, d] numbers of `dtype` with strides (in numbers) strides[0..2]
+ *   for B, H, N and 1 for d; any alignment, stride 0 included.
+ * positions: int32 [B, N, axes], strides pos_stride_b and pos_stride_n (0 to
+ *   repeat), 1 for the axes.  Computed in fp32, rounded once.
+ * out: contiguous [B, H, N, d], no overlap with x.  B, H or N of 0: no-op.
+ * INVALID_ARG for null pointers, 2 * pairs > d, axes < 1, magnitude <= 0;
+ * UNSUPPORTED for another dtype.  Asynchronous.
+ */
+mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, const int64_t *strides,
+                      const int32_t *positions, int64_t pos_stride_b, int64_t pos_stride_n,
+                      const mcs_rotary *rotary, int back, void *out, mcs_stream_t stream);
+
+/* A paged cache of keys and values in e4m3 (e4m3fn), all device memory owned
+ * by the caller.  Token j of sequence b lies in page page_table[b, j / page],
+ * slot j % page.  A stored number stands for e4m3 * scale of its page and head
+ * (scales are positive; append writes powers of two).  Table entries behind a
+ * sequence's last page are never read.  An entry outside [0, n_pages) that is
+ * needed records MCS_ERR_BAD_META in the status word and is never followed:
+ * append writes nothing there, read gives zeros, attention leaves the page's
+ * tokens out.
+ * d in {64, 128}, page in {16, 32, 64, 128} (UNSUPPORTED otherwise);
+ * max_pages * page <= 2^30, n_pages * H * page < 2^31, B * H <= 65535, pages
+ * 16-byte aligned (INVALID_ARG otherwise). */
+typedef struct {
+  void *k_pages, *v_pages;   /* [n_pages, H, page, d] e4m3 */
+  float *k_scale, *v_scale;  /* [n_pages, H]               */
+  const int32_t *page_table; /* [B, max_pages]             */
+  int32_t n_pages, max_pages, B, H, page, d;
+} mcs_cache;
+
+/*
+ * mcs_cache_append -- tokens start[b] .. start[b] + counts[b] - 1 of each
+ * sequence from K, V (bf16 [B, H, n, d], strides in numbers for B, H, n,
+ * multiples of 8; 1 for d; 16-byte aligned).  counts int32 [B] (clamped to
+ * [0, n]) or NULL: n each.  With `rotary` the keys turn by `positions` (int32
+ * [B, n, axes], strides as in mcs_rotate), or by their place start[b] + i when
+ * positions is NULL (axes must be 1 then); rotated numbers are rounded once,
+ * to e4m3.  In the half layout pairs must be a multiple of 8 (UNSUPPORTED).
+ * Each touched (page, head) gets the smallest scale 2^e, |e| <= 60, that fits
+ * its new numbers; where the page holds earlier tokens of the sequence (places
+ * below start[b]) the scale never falls and they move to it.  What lay at
+ * places from start[b] + counts[b] on in the last page is no longer valid: a
+ * call sets the sequence's end.  +-inf is held as +-448 * scale; a token with
+ * a NaN in its (rotated) key or value of a head has its key there held as NaN
+ * and the value's NaN as 0.
+ * start[b] < 0, or a place behind the table: nothing is written there and
+ * MCS_ERR_BAD_META is recorded.  A page may be touched for one sequence only
+ * in a call.  n == 0 is a no-op.  Asynchronous.
+ */
+mcs_status mcs_cache_append(const mcs_cache *cache, const void *K, const void *V, const int64_t *k_strides,
+                            const int64_t *v_strides, int n, const int32_t *start, const int32_t *counts,
+                            const int32_t *positions, int64_t pos_stride_b, int64_t pos_stride_n,
+                            const mcs_rotary *rotary, mcs_stream_t stream);
+
+/* mcs_cache_read -- tokens start[b] .. start[b] + n - 1 of each sequence as
+ * bf16 [B, H, n, d] (what the held numbers stand for, exact for power-of-two
+ * scales): the layout mcs_plan and mcs_dense take.  Rows from counts[b] on
+ * (counts int32 [B], may be NULL), at negative places and behind the table are
+ * zeros.  n == 0 is a no-op.  Asynchronous. */
+mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const int32_t *counts, int n, void *K, void *V,
+                          mcs_stream_t stream);
+
+/*
+ * mcs_cache_attention -- O = softmax(scale Q K^T) V over the cache's tokens
+ * [0, lengths[b]) of each sequence.
+ * Q, O: bf16 [B, Hq, Nq, d], contiguous, 16-byte aligned; Hq a multiple of
+ *   H: query head h goes by key head h / (Hq / H).  Nq * Hq / H <= 2^20.
+ * lengths: int32 [B]; more than the table holds counts as what it holds and
+ *   records MCS_ERR_BAD_META.
+ * counts: int32 [B] query tokens of each sequence (rows from counts[b] on give
+ *   zeros), or NULL: Nq each.
+ * causal: query i of a sequence stands at place lengths[b] - counts[b] + i and
+ *   sees the places up to its own; else every query sees all.
+ * lse: float32 [B, Hq, Nq] or NULL: log of the sum of exp of a row's scores.
+ * A row that sees nothing gives zeros, and -inf in lse.  Weights and products:
+ * fp32 sums and statistics of exact 8-bit numbers and 16-bit weights.
+ * Nq == 0 is a no-op.  Needs no workspace; repeats bit for bit.  Asynchronous.
+ */
+mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, int Nq, const int32_t *lengths,
+                               const int32_t *counts, int causal, float scale, void *O, float *lse,
+                               mcs_stream_t stream);
+
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns MCS_OK, or MCS_ERR_TIMEOUT if a kernel's bounded wait ran out
  * since the last read. */

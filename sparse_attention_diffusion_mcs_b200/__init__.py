@@ -33,3 +33,5 @@ from .api import (  # noqa: F401
     workspace_views,
 )
 from .denoise import Schedule, fidelity  # noqa: F401,E402
+from .rotary import Rotary, rotate  # noqa: F401,E402
+from .cache import KVCache, cache_append, cache_attention, cache_read  # noqa: F401,E402

@@ -31,7 +31,22 @@ class McsMeta(ctypes.Structure):
                 ("pair_idx", c_vp), ("pair_len", c_vp)]
 
 
+class McsRotary(ctypes.Structure):
+    _fields_ = [("turns", c_vp), ("axis", c_vp), ("pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("magnitude", c_float)]
+
+
+class McsCache(ctypes.Structure):
+    _fields_ = [("k_pages", c_vp), ("v_pages", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("page_table", c_vp),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("page", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
 PMETA = ctypes.POINTER(McsMeta)
+PROTARY = ctypes.POINTER(McsRotary)
+PCACHE = ctypes.POINTER(McsCache)
+c_i64 = ctypes.c_int64
+PI64 = ctypes.POINTER(c_i64)
 
 PROTOTYPES = {
     "mcs_abi_version": (c_int, []),
@@ -67,6 +82,12 @@ PROTOTYPES = {
     "mcs_union_pairs": (c_int, [c_vp, c_int, c_int, c_int, c_int, c_vp, c_vp, c_vp]),
     "mcs_sparse_step_blocks": (c_int, [c_vp, c_vp, c_vp, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                        c_vp, c_vp, c_vp, c_vp, c_float, c_vp, c_vp]),
+    "mcs_rotate": (c_int, [c_vp, c_int, c_int, c_int, c_int, c_int, PI64, c_vp, c_i64, c_i64, PROTARY, c_int, c_vp,
+                           c_vp]),
+    "mcs_cache_append": (c_int, [PCACHE, c_vp, c_vp, PI64, PI64, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, PROTARY,
+                                 c_vp]),
+    "mcs_cache_read": (c_int, [PCACHE, c_vp, c_vp, c_int, c_vp, c_vp, c_vp]),
+    "mcs_cache_attention": (c_int, [PCACHE, c_vp, c_int, c_int, c_vp, c_vp, c_int, c_float, c_vp, c_vp, c_vp]),
     "mcs_last_device_status": (c_int, [c_vp]),
     "mcs_selftest_wait_timeout": (c_int, [c_u64, c_vp]),
     "mcs_set_wait_limit_ns": (None, [c_u64]),

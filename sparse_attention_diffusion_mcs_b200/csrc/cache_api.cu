@@ -1,0 +1,303 @@
+// cache_api.cu -- host side of the rotary and cache entry points of
+// include/mcs.h: argument checks and launches on the caller's stream.
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/mcs.h"
+#include "cache_rows_kernel.cuh"
+#include "host_shared.h"
+#include "kvcache_kernels.cuh"
+#include "rotary.cuh"
+
+using namespace mcs;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+mcs_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MCS_OK : MCS_ERR_CUDA; }
+cudaStream_t cu(mcs_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+struct Device {
+  int id = -1, sms = 0;
+};
+// the current device and its number of SMs (asked once per device)
+bool current_device(Device *d) {
+  static std::atomic<int> sms[kMaxDevices];
+  if (cudaGetDevice(&d->id) != cudaSuccess || d->id < 0 || d->id >= kMaxDevices) return false;
+  d->sms = sms[d->id].load(std::memory_order_relaxed);
+  if (!d->sms) {
+    if (cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess) return false;
+    sms[d->id].store(d->sms, std::memory_order_relaxed);
+  }
+  return true;
+}
+
+// a kernel's dynamic shared memory limit, set once per device
+template <auto *Kernel>
+cudaError_t allow_smem(const Device &d, int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = 1ull << d.id;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+mcs_status check_rotary(const mcs_rotary *r, int d, RotaryTable *t) {
+  std::memset(t, 0, sizeof(*t));
+  t->mag = 1.f;
+  if (!r) return MCS_OK;
+  if (r->pairs < 0 || 2ll * r->pairs > d || r->axes < 1) return MCS_ERR_INVALID_ARG;
+  if (!(r->magnitude > 0.f) || !std::isfinite(r->magnitude)) return MCS_ERR_INVALID_ARG;
+  if (r->pairs > 0 && (!r->turns || !r->axis || (reinterpret_cast<uintptr_t>(r->turns) & 7u) || !aligned4(r->axis)))
+    return MCS_ERR_INVALID_ARG;
+  t->turns = reinterpret_cast<const unsigned long long *>(r->turns);
+  t->axis = r->axis;
+  t->pairs = r->pairs;
+  t->interleaved = r->interleaved != 0;
+  t->axes = r->axes;
+  t->mag = r->magnitude;
+  return MCS_OK;
+}
+
+mcs_status check_cache(const mcs_cache *c, CacheView *v) {
+  if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->page_table) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
+      !aligned4(c->page_table))
+    return MCS_ERR_INVALID_ARG;
+  if (c->B < 1 || c->H < 1 || c->n_pages < 1 || c->max_pages < 1) return MCS_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return MCS_ERR_UNSUPPORTED;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MCS_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->B) * c->H > 65535) return MCS_ERR_INVALID_ARG;
+  if (static_cast<long long>(c->max_pages) * c->page > (1ll << 30)) return MCS_ERR_INVALID_ARG;
+  // TMA row coordinates are int32
+  if (static_cast<long long>(c->n_pages) * c->H > (1ll << 31) / c->page - 1) return MCS_ERR_INVALID_ARG;
+  v->k = static_cast<uint8_t *>(c->k_pages);
+  v->v = static_cast<uint8_t *>(c->v_pages);
+  v->k_scale = c->k_scale;
+  v->v_scale = c->v_scale;
+  v->table = c->page_table;
+  v->n_pages = c->n_pages;
+  v->max_pages = c->max_pages;
+  v->H = c->H;
+  v->page = c->page;
+  v->d = c->d;
+  return MCS_OK;
+}
+
+// ---------------------------------------------------------------- rotate
+template <typename T>
+cudaError_t launch_rotate(RotateArgs &a, bool vec, const Device &dev, cudaStream_t s) {
+  const long long per_token = vec ? a.d / 16 : a.d - a.t.pairs;
+  const long long threads = static_cast<long long>(a.B) * a.N * per_token;
+  const long long blocks = (threads + kRotateThreads - 1) / kRotateThreads;
+  // A thread walks over a group of heads with one set of angles.  Few tokens:
+  // smaller groups, down to one head, until the grid has 1024 threads per SM.
+  const long long want = 1024ll * dev.sms / kRotateThreads;
+  long long groups = (want + blocks - 1) / blocks;
+  groups = groups < 1 ? 1 : (groups > a.H ? a.H : groups);
+  a.heads = static_cast<int>((a.H + groups - 1) / groups);
+  const dim3 grid(static_cast<unsigned>(blocks), (a.H + a.heads - 1) / a.heads);
+  if (vec)
+    rotate_kernel<T, true><<<grid, kRotateThreads, 0, s>>>(a);
+  else
+    rotate_kernel<T, false><<<grid, kRotateThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- attention over the cache
+template <int D, int MT>
+cudaError_t launch_rows(CacheAttnArgs &a, const Device &dev, cudaStream_t s) {
+  using C = RowsCfg<D, MT>;
+  static_assert(C::SMEM * (MT == 1 ? 2 : 1) <= 232448, "shared memory budget");
+  cudaError_t e = allow_smem<cache_rows_kernel<D, MT>>(dev, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(a.Nq) * a.share;
+  const long long blocks = (rows + 16 * MT - 1) / (16 * MT);
+  if (blocks > 65535) return cudaErrorInvalidValue;
+  // One cluster per (sequence, key head, block of rows), its CTAs sharing the
+  // key tiles: as many as fill the SMs once, 8 (the portable size) at most,
+  // and no more than there can be tiles.
+  const long long items = static_cast<long long>(a.B) * a.c.H * blocks;
+  const long long tiles = (static_cast<long long>(a.c.max_pages) * a.c.page + C::BN - 1) / C::BN;
+  long long split = static_cast<long long>(dev.sms) * (MT == 1 ? 2 : 1) / items;
+  split = split > 8 ? 8 : split;
+  split = split > tiles ? tiles : split;
+  split = split < 1 ? 1 : split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split), static_cast<unsigned>(a.B * a.c.H), static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(split);
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<D, MT>, a);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- the C ABI
+extern "C" {
+
+mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, const int64_t *strides,
+                      const int32_t *positions, int64_t pos_stride_b, int64_t pos_stride_n, const mcs_rotary *rotary,
+                      int back, void *out, mcs_stream_t stream) {
+  if (!rotary || !strides || B < 0 || H < 0 || N < 0 || d < 1) return MCS_ERR_INVALID_ARG;
+  if (dtype != MCS_BF16 && dtype != MCS_FP16 && dtype != MCS_FP32) return MCS_ERR_UNSUPPORTED;
+  RotateArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const mcs_status st = check_rotary(rotary, d, &a.t);
+  if (st != MCS_OK) return st;
+  if (B == 0 || H == 0 || N == 0) return MCS_OK;
+  if (!x || !out || !positions || !aligned4(positions)) return MCS_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N > INT_MAX || H > INT_MAX / d) return MCS_ERR_INVALID_ARG;
+  if (static_cast<double>(B) * N * d > 5e11) return MCS_ERR_INVALID_ARG;   // the grid's x is below 2^31 blocks
+  const int elt = dtype == MCS_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % elt || reinterpret_cast<uintptr_t>(out) % elt) return MCS_ERR_INVALID_ARG;
+  a.x = x;
+  a.out = out;
+  a.pos = positions;
+  a.pos_b = pos_stride_b;
+  a.pos_n = pos_stride_n;
+  // a dimension of one entry has no stride
+  a.sb = B > 1 ? strides[0] : 0;
+  a.sh = H > 1 ? strides[1] : 0;
+  a.sn = N > 1 ? strides[2] : 0;
+  a.B = B;
+  a.H = H;
+  a.N = N;
+  a.d = d;
+  a.back = back != 0;
+  // 16-byte vectors need whole units of 16 numbers and aligned rows
+  const bool vec = d % 16 == 0 && (a.t.interleaved || a.t.pairs % 8 == 0) && aligned16(x) && aligned16(out) &&
+                   a.sb * elt % 16 == 0 && a.sh * elt % 16 == 0 && a.sn * elt % 16 == 0;
+  Device dev;
+  if (!current_device(&dev)) return MCS_ERR_CUDA;
+  const cudaError_t e = dtype == MCS_FP32   ? launch_rotate<float>(a, vec, dev, cu(stream))
+                        : dtype == MCS_FP16 ? launch_rotate<__half>(a, vec, dev, cu(stream))
+                                            : launch_rotate<bf16>(a, vec, dev, cu(stream));
+  return cuda_status(e);
+}
+
+mcs_status mcs_cache_append(const mcs_cache *cache, const void *K, const void *V, const int64_t *k_strides,
+                            const int64_t *v_strides, int n, const int32_t *start, const int32_t *counts,
+                            const int32_t *positions, int64_t pos_stride_b, int64_t pos_stride_n,
+                            const mcs_rotary *rotary, mcs_stream_t stream) {
+  AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  mcs_status st = check_cache(cache, &a.c);
+  if (st != MCS_OK) return st;
+  st = check_rotary(rotary, a.c.d, &a.t);
+  if (st != MCS_OK) return st;
+  if (n < 0 || !k_strides || !v_strides) return MCS_ERR_INVALID_ARG;
+  if (!a.t.interleaved && a.t.pairs % 8 != 0) return MCS_ERR_UNSUPPORTED;
+  if (!positions && a.t.pairs > 0 && a.t.axes != 1) return MCS_ERR_INVALID_ARG;
+  if (n == 0) return MCS_OK;
+  if (!K || !V || !start || !aligned16(K) || !aligned16(V) || !aligned4(start) || !aligned4(counts) ||
+      !aligned4(positions))
+    return MCS_ERR_INVALID_ARG;
+  if (n > (1 << 30) || a.c.H > 65535 || cache->B > 65535) return MCS_ERR_INVALID_ARG;
+  const int sizes[3] = {cache->B, a.c.H, n};
+  long long ks[3], vs[3];
+  for (int i = 0; i < 3; ++i) {
+    ks[i] = sizes[i] > 1 ? k_strides[i] : 0;
+    vs[i] = sizes[i] > 1 ? v_strides[i] : 0;
+    if (ks[i] % 8 || vs[i] % 8) return MCS_ERR_INVALID_ARG;   // rows on 16-byte boundaries
+  }
+  a.K = static_cast<const bf16 *>(K);
+  a.V = static_cast<const bf16 *>(V);
+  a.k_sb = ks[0], a.k_sh = ks[1], a.k_sn = ks[2];
+  a.v_sb = vs[0], a.v_sh = vs[1], a.v_sn = vs[2];
+  a.start = start;
+  a.counts = counts;
+  a.pos = positions;
+  a.pos_b = pos_stride_b;
+  a.pos_n = pos_stride_n;
+  a.n = n;
+  if (!(a.status = device_status_word())) return MCS_ERR_CUDA;
+  // n tokens reach into ceil((n - 1) / page) + 1 pages at most
+  const dim3 grid((n + a.c.page - 2) / a.c.page + 1, a.c.H, cache->B);
+  const int units = a.c.page * (a.c.d / 16);
+  if (units <= kAppendThreads)
+    append_kernel<1><<<grid, kAppendThreads, 0, cu(stream)>>>(a);
+  else if (units <= 2 * kAppendThreads)
+    append_kernel<2><<<grid, kAppendThreads, 0, cu(stream)>>>(a);
+  else
+    append_kernel<4><<<grid, kAppendThreads, 0, cu(stream)>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const int32_t *counts, int n, void *K, void *V,
+                          mcs_stream_t stream) {
+  ReadArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const mcs_status st = check_cache(cache, &a.c);
+  if (st != MCS_OK) return st;
+  if (n < 0) return MCS_ERR_INVALID_ARG;
+  if (n == 0) return MCS_OK;
+  if (!K || !V || !start || !aligned16(K) || !aligned16(V) || !aligned4(start) || !aligned4(counts))
+    return MCS_ERR_INVALID_ARG;
+  a.start = start;
+  a.counts = counts;
+  a.K = static_cast<bf16 *>(K);
+  a.V = static_cast<bf16 *>(V);
+  a.n = n;
+  a.units = static_cast<long long>(cache->B) * a.c.H * n * (a.c.d / 16);
+  const long long blocks = (a.units + kReadThreads - 1) / kReadThreads;
+  if (blocks > INT_MAX) return MCS_ERR_INVALID_ARG;
+  if (!(a.status = device_status_word())) return MCS_ERR_CUDA;
+  cache_read_kernel<<<static_cast<unsigned>(blocks), kReadThreads, 0, cu(stream)>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, int Nq, const int32_t *lengths,
+                               const int32_t *counts, int causal, float scale, void *O, float *lse,
+                               mcs_stream_t stream) {
+  CacheAttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const mcs_status st = check_cache(cache, &a.c);
+  if (st != MCS_OK) return st;
+  if (Hq < 1 || Hq % a.c.H != 0 || Nq < 0) return MCS_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return MCS_ERR_INVALID_ARG;
+  if (Nq == 0) return MCS_OK;
+  if (!Q || !O || !lengths || !aligned16(Q) || !aligned16(O) || !aligned4(lengths) || !aligned4(counts) || !aligned4(lse))
+    return MCS_ERR_INVALID_ARG;
+  if (static_cast<long long>(Nq) * (Hq / a.c.H) > (1 << 20)) return MCS_ERR_INVALID_ARG;
+  a.Q = static_cast<const bf16 *>(Q);
+  a.O = static_cast<bf16 *>(O);
+  a.lse = lse;
+  a.lengths = lengths;
+  a.counts = counts;
+  a.B = cache->B;
+  a.Hq = Hq;
+  a.Nq = Nq;
+  a.share = Hq / a.c.H;
+  a.causal = causal != 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = wait_limit_ns();
+  Device dev;
+  if (!current_device(&dev) || !(a.status = device_status_word())) return MCS_ERR_CUDA;
+  const size_t rows = static_cast<size_t>(a.c.n_pages) * a.c.H * a.c.page;
+  if (!map_byte_rows(&a.tmK, a.c.k, a.c.d, rows, a.c.page) || !map_byte_rows(&a.tmV, a.c.v, a.c.d, rows, a.c.page))
+    return MCS_ERR_CUDA;
+  const bool one = static_cast<long long>(Nq) * a.share <= 16;
+  cudaError_t e;
+  if (a.c.d == 64)
+    e = one ? launch_rows<64, 1>(a, dev, cu(stream)) : launch_rows<64, 2>(a, dev, cu(stream));
+  else
+    e = one ? launch_rows<128, 1>(a, dev, cu(stream)) : launch_rows<128, 2>(a, dev, cu(stream));
+  return cuda_status(e);
+}
+
+}  // extern "C"

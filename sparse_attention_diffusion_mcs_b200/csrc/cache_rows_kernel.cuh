@@ -1,0 +1,520 @@
+// cache_rows_kernel.cuh -- attention of few query rows over the 8-bit cache
+// (single tokens, short drafts): bound by reading the cache once.
+//
+// For row i and token j of the page with scales ks, vs (base-2 units):
+//   x_ij = scale log2(e) (q_i . k8_j) ks,     y_ij = x_ij + log2(vs),
+//   O_i  = sum_j 2^(y_ij - m_i) v8_j  /  sum_j 2^(y_ij - m_i) / vs,
+// m_i the running maximum of y.  2^y = 2^x vs is the weight that v8 itself
+// gets, so the held numbers enter the products as they are (e4m3 is exact in
+// fp16), every weight is <= 1 whatever the pages' scales, and no page is
+// dequantised.  m, the sums and O are fp32; the weights are rounded to fp16
+// (2^-11 relative; below 2^-14 of the row's largest weight, an absolute 2^-25).
+// Queries are held as fp16 of q 2^-e, 2^e the power of two at the row's
+// largest magnitude: exact for bf16 numbers down to 2^-17 of it, and off by
+// 2^-25 of it below.
+//
+// A CTA takes 16 MT rows -- all query heads that share a key head, times their
+// tokens -- and a run of 128-key tiles; a cluster of C CTAs takes a whole
+// sequence, each CTA its share of the tiles, and merges (m, l, O) through
+// distributed shared memory: no workspace and no second launch, and the merge
+// order is fixed, so results repeat bit for bit.
+// Products by mma.sync m16n8k16: one row tile of 16 is all there is, while a
+// tcgen05 product has at least 64 rows, needs its operands in 16 bits in
+// shared memory (an extra write and read of every number), and 16 rows
+// keep the tensor work far below the time of the bytes.
+//
+// Warps 0-3 each take 32 keys of every tile with their own online softmax
+// (no barrier between them until the end); warp 4 loads: one TMA box per page,
+// keys and values, into a ring of stages.  The swizzle of the boxes and the
+// order in which keys are dealt to the product's columns keep every shared
+// memory read free of bank conflicts (key_of below).
+#pragma once
+
+#include "kvcache_kernels.cuh"
+
+namespace mcs {
+
+struct CacheAttnArgs {
+  CUtensorMap tmK, tmV;          // [n_pages * H * page, d] bytes, box min(page, 128) rows
+  CacheView c;
+  const bf16 *Q;                 // [B, Hq, Nq, d]
+  bf16 *O;                       // [B, Hq, Nq, d]
+  float *lse;                    // [B, Hq, Nq] or null: log of the sum of exp (natural units)
+  const int32_t *lengths;        // [B] tokens kept
+  const int32_t *counts;         // [B] query tokens, or null: Nq
+  int B, Hq, Nq, share;          // share = Hq / H
+  int causal;
+  float scale_log2;
+  unsigned *status;
+  unsigned long long wait_ns;
+};
+
+template <int D, int MT>
+struct RowsCfg {
+  static constexpr int BN = 128;                       // keys per tile
+  static constexpr int TILE = BN * D;                  // bytes of a K or V tile
+  static constexpr int NS = (D == 128 ? 3 : 6) * (MT == 1 ? 1 : 2);
+  static constexpr int OFF_KV = 0;
+  static constexpr int OFF_SC = OFF_KV + NS * 2 * TILE;   // per stage: 8 x float4 (ks, log2 vs, 1 / vs, -)
+  static constexpr int OFF_BAR = OFF_SC + NS * 8 * 16;
+  static constexpr int OFF_ML = OFF_BAR + 16 * NS;        // merged (m, l) of 16 MT rows
+  static constexpr int OFF_WML = OFF_ML + 16 * MT * 8;    // per warp (m, l)
+  static constexpr int OFF_MISC = OFF_WML + 4 * 16 * MT * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  // after the last tile, over the ring: the warps' O, then the CTA's merged O
+  static constexpr int OLD = D + 4;
+  static constexpr int OFF_WO = 0;
+  static constexpr int OFF_O = OFF_WO + 4 * 16 * MT * OLD * 4;
+  static_assert(OFF_O + 16 * MT * D * 4 <= OFF_SC, "the merge fits the ring");
+  static constexpr int THREADS = 5 * 32;
+};
+
+// The key (of eight) in column `col` of a score tile.  A quarter warp reads the
+// 16-byte chunks t = 0..3 of the keys of two neighbouring columns (scores), or
+// chunks g, g + 1 of the keys of columns u, 2 + u, 4 + u, 6 + u (P.V): the order
+// sends each of these to different banks under the boxes' swizzle.
+// d = 128 (128B): 0 5 2 7 4 1 6 3; d = 64 (64B): 0 3 1 2 4 7 5 6.
+template <int D>
+__device__ __forceinline__ int key_of(int col) {
+  if (D == 128) return col & 1 ? col ^ 4 : col;
+  const int base = (col >> 2) * 4 + ((col >> 1) & 1);
+  return col & 1 ? base ^ 3 : base;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float ld_dsmem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(r)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
+    cache_rows_kernel(const __grid_constant__ CacheAttnArgs a) {
+  using C = RowsCfg<D, MT>;
+  constexpr int NS = C::NS, BN = C::BN, SEG = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto b_full = [&](int s) { return bar0 + 8 * s; };
+  auto b_empty = [&](int s) { return bar0 + 8 * (NS + s); };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
+
+  const CacheView &cv = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x, ranks = gridDim.x;        // the cluster spans the x dimension
+  const int b = blockIdx.y / cv.H, h = blockIdx.y - b * cv.H;
+  const int row0 = blockIdx.z * 16 * MT;                 // rows are (token, query head of the group)
+  const int n_rows = a.Nq * a.share;
+  const long long cap = static_cast<long long>(cv.max_pages) * cv.page;
+  int len = a.lengths[b];
+  if (len > cap) {
+    if (tid == 0) record_status(a.status, kStatusBadMeta);
+    len = static_cast<int>(cap);
+  }
+  len = max(len, 0);
+  const int nq = a.counts ? min(max(a.counts[b], 0), a.Nq) : a.Nq;
+  // keys that row i of the sequence sees: [0, limit)
+  auto limit_of = [&](int row) {
+    const int i = row / a.share;
+    if (row >= n_rows || i >= nq) return 0;
+    return a.causal ? max(len - nq + i + 1, 0) : len;
+  };
+  const int last_row = min(row0 + 16 * MT, n_rows) - 1;
+  const int last_query = min(last_row, nq * a.share - 1);
+  const int kmax = last_query < row0 ? 0 : limit_of(last_query);   // later rows see no less
+  const int tiles = (kmax + BN - 1) / BN;
+  const int t0 = static_cast<int>(static_cast<long long>(tiles) * rank / ranks);
+  const int t1 = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / ranks);
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(b_full(s), 1);
+      mbar_init(b_empty(s), 4);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ loads
+    // lane l holds page and scales of the 16-key group 32 bt + l of batch bt
+    // (four tiles); the next batch's are on the way meanwhile
+    if (lane == 0) {
+      tma_prefetch_desc(&a.tmK);
+      tma_prefetch_desc(&a.tmV);
+    }
+    const int32_t *table = cv.table + static_cast<long long>(b) * cv.max_pages;
+    const int groups = (kmax + 15) / 16;
+    auto fetch_page = [&](int g) {
+      int p = -1;
+      if (g < groups) {
+        p = table[g * 16 / cv.page];
+        if (p < 0 || p >= cv.n_pages) {
+          record_status(a.status, kStatusBadMeta);
+          p = -1;
+        }
+      }
+      return p;
+    };
+    int pid = fetch_page(8 * t0 + lane);
+    float ks = 0.f, vs = 0.f;
+    auto fetch_scales = [&](int p, float &k, float &v) {
+      k = v = 0.f;
+      if (p >= 0) {
+        k = cv.k_scale[static_cast<size_t>(p) * cv.H + h];
+        v = cv.v_scale[static_cast<size_t>(p) * cv.H + h];
+      }
+    };
+    fetch_scales(pid, ks, vs);
+    bool ok = true;
+    int issued = 0;
+    const int gpb = cv.page / 16;                    // groups per page (a page is at most a tile)
+    for (int tb = t0; tb < t1 && ok; tb += 4) {
+      const int npid = fetch_page(8 * (tb + 4) + lane);
+      float nks, nvs;
+      fetch_scales(npid, nks, nvs);
+      for (int t = tb; t < min(tb + 4, t1); ++t) {
+        const int it = t - t0, s = it % NS;
+        const int gl = 8 * (t - tb);                 // lane of the tile's first group
+        ok = mbar_wait_warp(b_empty(s), ((it / NS) & 1) ^ 1, a.wait_ns, abort_flag);
+        if (!ok) break;
+        if (lane >= gl && lane < gl + 8) {
+          float4 f;
+          f.x = ks;
+          f.y = pid >= 0 ? __log2f(vs) : -INFINITY;
+          f.z = pid >= 0 ? 1.f / vs : 0.f;
+          f.w = 0.f;
+          *reinterpret_cast<float4 *>(smem + C::OFF_SC + (s * 8 + lane - gl) * 16) = f;
+        }
+        // the first lane of each page's groups loads it
+        const bool mine = lane >= gl && lane < gl + 8 && (lane - gl) % gpb == 0 && pid >= 0;
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        const uint32_t page_bytes = static_cast<uint32_t>(cv.page) * D;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(b_full(s), __popc(who) * 2 * page_bytes);
+        __syncwarp();
+        if (mine) {
+          const uint32_t dst = sbase + C::OFF_KV + s * 2 * C::TILE + (lane - gl) * 16 * D;
+          const int r = static_cast<int>((static_cast<long long>(pid) * cv.H + h) * cv.page);
+          tma_load_2d(dst, &a.tmK, 0, r, b_full(s));
+          tma_load_2d(dst + C::TILE, &a.tmV, 0, r, b_full(s));
+        }
+        __syncwarp();
+        ++issued;
+      }
+      pid = npid;
+      ks = nks;
+      vs = nvs;
+    }
+    if (!ok && lane == 0 && !*abort_flag) {
+      *abort_flag = 1;
+      record_status(a.status, kStatusTimeout);
+    }
+    // never leave the CTA with a copy still landing in its shared memory
+    volatile int never = 0;
+    for (int it = (issued > NS ? issued - NS : 0); it < issued; ++it)
+      mbar_wait(b_full(it % NS), (it / NS) & 1, 2000000000ull, &never);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ products and softmax
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t qa[MT][SEG][4][4];
+    float rowf[MT][2];
+    int lim[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = row0 + mt * 16 + u * 8 + g;
+        lim[mt][u] = limit_of(row);
+        uint4 w[SEG][2];
+#pragma unroll
+        for (int sg = 0; sg < SEG; ++sg) w[sg][0] = w[sg][1] = make_uint4(0, 0, 0, 0);
+        if (row < n_rows) {
+          const int i = row / a.share, hq = h * a.share + row % a.share;
+          const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + ((static_cast<size_t>(b) * a.Hq + hq) * a.Nq + i) * D);
+#pragma unroll
+          for (int sg = 0; sg < SEG; ++sg) {
+            w[sg][0] = q[sg * 8 + 2 * t];
+            w[sg][1] = q[sg * 8 + 2 * t + 1];
+          }
+        }
+        // the row's largest magnitude, as bf16 bits
+        uint32_t am = 0;
+        const uint32_t *x = reinterpret_cast<const uint32_t *>(w);
+#pragma unroll
+        for (int i = 0; i < SEG * 8; ++i) am = max(am, max((x[i] << 1) & 0xFFFEu, (x[i] >> 15) & 0xFFFEu));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        rowf[mt][u] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int sg = 0; sg < SEG; ++sg) {
+          const uint32_t *y = reinterpret_cast<const uint32_t *>(w[sg]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const uint32_t z = y[2 * j + p];
+              qa[mt][sg][j][u + 2 * p] =
+                  half2_bits(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
+            }
+        }
+      }
+    // keys every row of the CTA sees
+    int all = 0x7FFFFFFF;
+    for (int row = row0; row <= last_row; ++row) all = min(all, limit_of(row));
+
+    constexpr int NT = D / 8;          // column tiles of O
+    float o[MT][NT][4];
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][c][e] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+    bool ok = true;
+    for (int tt = t0; tt < t1; ++tt) {
+      const int it = tt - t0, s = it % NS;
+      if (!mbar_wait_warp(b_full(s), (it / NS) & 1, a.wait_ns, abort_flag)) {
+        ok = false;
+        break;
+      }
+      const int key0 = tt * BN + warp * 32;
+      if (key0 < kmax) {
+        const uint8_t *kb = smem + C::OFF_KV + s * 2 * C::TILE + warp * 32 * D;
+        const uint8_t *vb = kb + C::TILE;
+        const float4 *scp = reinterpret_cast<const float4 *>(smem + C::OFF_SC) + s * 8 + warp * 2;
+        const float4 sc0 = scp[0], sc1 = scp[1];
+        const bool clean = key0 + 32 <= all && sc0.y > -INFINITY && sc1.y > -INFINITY;
+        // ---- scores of 32 keys
+        float sc[MT][4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][i][e] = 0.f;
+          const int r = 8 * i + key_of<D>(g);
+#pragma unroll
+          for (int sg = 0; sg < SEG; ++sg) {
+            const int chunk = D == 128 ? ((4 * sg + t) ^ (r & 7)) : (t ^ ((r >> 1) & 3));
+            const uint4 w = *reinterpret_cast<const uint4 *>(kb + r * D + chunk * 16);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t b0 = half2_of_e4m3x2(x[j]), b1 = half2_of_e4m3x2_hi(x[j]);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma_f16(sc[mt][i], qa[mt][sg][j][0], qa[mt][sg][j][1], qa[mt][sg][j][2], qa[mt][sg][j][3], b0, b1);
+            }
+          }
+        }
+        // ---- online softmax; column 2t + u of group i is key key0 + 8 i + key_of(2t + u)
+        uint32_t pa[MT][4][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = i < 2 ? sc0 : sc1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float y = fmaf(sc[mt][i][e], rowf[mt][e >> 1] * f.x, f.y);
+              if (!clean) {
+                const int key = key0 + 8 * i + key_of<D>(2 * t + (e & 1));
+                y = key < lim[mt][e >> 1] && f.y > -INFINITY ? y : -INFINITY;
+              }
+              sc[mt][i][e] = y;
+              mx[e >> 1] = fmaxf(mx[e >> 1], y);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+            mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+          }
+          if (__any_sync(0xffffffffu, mx[0] > m[mt][0] || mx[1] > m[mt][1])) {
+            float al[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float nm = fmaxf(m[mt][u], mx[u]);
+              al[u] = nm == m[mt][u] ? 1.f : ex2_approx(m[mt][u] - nm);
+              m[mt][u] = nm;
+              l[mt][u] *= al[u];
+            }
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+              o[mt][c][0] *= al[0];
+              o[mt][c][1] *= al[0];
+              o[mt][c][2] *= al[1];
+              o[mt][c][3] *= al[1];
+            }
+          }
+          const float mu[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0], m[mt][1] == -INFINITY ? 0.f : m[mt][1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float inv = i < 2 ? sc0.z : sc1.z;
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = ex2_approx(sc[mt][i][e] - mu[e >> 1]);
+            l[mt][0] = fmaf(p[0] + p[1], inv, l[mt][0]);
+            l[mt][1] = fmaf(p[2] + p[3], inv, l[mt][1]);
+            pa[mt][i][0] = half2_bits(p[0], p[1]);
+            pa[mt][i][1] = half2_bits(p[2], p[3]);
+          }
+        }
+        // ---- P.V; column g of tile c is number (D / 8) g + c
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii) {
+          uint4 w[4];   // D / 8 bytes of the keys of columns 2t, 2t + 1, of groups 2 ii and 2 ii + 1
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 16 * ii + 8 * (q >> 1) + key_of<D>(2 * t + (q & 1));
+            if (D == 128) {
+              w[q] = *reinterpret_cast<const uint4 *>(vb + r * D + ((g ^ (r & 7)) * 16));
+            } else {
+              const uint2 z = *reinterpret_cast<const uint2 *>(vb + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16) + (g & 1) * 8);
+              w[q] = make_uint4(z.x, z.y, 0, 0);
+            }
+            // what lies behind the last token, or was never loaded, may be any bits
+            const float lv = ii ? sc1.y : sc0.y;
+            if (!clean && !(key0 + r < kmax && lv > -INFINITY)) w[q] = make_uint4(0, 0, 0, 0);
+          }
+          const uint32_t x0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, x1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+          const uint32_t x2[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, x3[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
+#pragma unroll
+          for (int q = 0; q < NT / 4; ++q) {
+            const uint32_t lo0 = __byte_perm(x0[q], x1[q], 0x5140), lo1 = __byte_perm(x0[q], x1[q], 0x7362);
+            const uint32_t hi0 = __byte_perm(x2[q], x3[q], 0x5140), hi1 = __byte_perm(x2[q], x3[q], 0x7362);
+            const uint32_t b0[4] = {half2_of_e4m3x2(lo0), half2_of_e4m3x2_hi(lo0), half2_of_e4m3x2(lo1), half2_of_e4m3x2_hi(lo1)};
+            const uint32_t b1[4] = {half2_of_e4m3x2(hi0), half2_of_e4m3x2_hi(hi0), half2_of_e4m3x2(hi1), half2_of_e4m3x2_hi(hi1)};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma_f16(o[mt][4 * q + c], pa[mt][2 * ii][0], pa[mt][2 * ii][1], pa[mt][2 * ii + 1][0], pa[mt][2 * ii + 1][1],
+                        b0[c], b1[c]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_empty(s));
+    }
+    if (!ok && lane == 0 && !*abort_flag) {
+      *abort_flag = 1;
+      record_status(a.status, kStatusTimeout);
+    }
+    // all warps of the CTA have read their last tile before the ring is reused
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    float2 *wml = reinterpret_cast<float2 *>(smem + C::OFF_WML);
+    float *wo = reinterpret_cast<float *>(smem + C::OFF_WO);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float s = l[mt][u];
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        const int r = warp * 16 * MT + mt * 16 + u * 8 + g;
+        if (t == 0) wml[r] = make_float2(m[mt][u], s);
+        // numbers (D / 8)(2t + e) + c
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int c = 0; c < NT; c += 4)
+            *reinterpret_cast<float4 *>(wo + r * C::OLD + NT * (2 * t + e) + c) =
+                make_float4(o[mt][c][2 * u + e], o[mt][c + 1][2 * u + e], o[mt][c + 2][2 * u + e], o[mt][c + 3][2 * u + e]);
+      }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    // ---- the four warps' parts into the CTA's
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    float *oc = reinterpret_cast<float *>(smem + C::OFF_O);
+    for (int idx = tid; idx < 16 * MT * (D / 4); idx += 128) {
+      const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, wml[w * 16 * MT + r].x);
+      float ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 p = wml[w * 16 * MT + r];
+        const float f = p.x == -INFINITY && !(p.y != p.y) ? 0.f : ex2_approx(p.x - mm);
+        const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 16 * MT + r) * C::OLD + c);
+        ll = fmaf(p.y, f, ll);
+        acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+      }
+      *reinterpret_cast<float4 *>(oc + r * D + c) = acc;
+      if (c == 0) ml[r] = make_float2(mm, ll);
+    }
+  }
+  // ---------------------------------------------------------------------- merge over the cluster
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (!*abort_flag) {
+    const int rows_here = min(16 * MT, n_rows - row0);
+    for (int idx = rank * C::THREADS + tid; idx < rows_here * (D / 4); idx += ranks * C::THREADS) {
+      const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
+      float mm = -INFINITY;
+      for (int k = 0; k < ranks; ++k) mm = fmaxf(mm, ld_dsmem(sbase + C::OFF_ML + r * 8, k));
+      float ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < ranks; ++k) {
+        const float pm = ld_dsmem(sbase + C::OFF_ML + r * 8, k), pl = ld_dsmem(sbase + C::OFF_ML + r * 8 + 4, k);
+        const float f = pm == -INFINITY && !(pl != pl) ? 0.f : ex2_approx(pm - mm);
+        const float4 x = ld_dsmem4(sbase + C::OFF_O + (r * D + c) * 4, k);
+        ll = fmaf(pl, f, ll);
+        acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+      }
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;      // a row that sees nothing is 0
+      const int row = row0 + r, i = row / a.share, hq = h * a.share + row % a.share;
+      const size_t at = (static_cast<size_t>(b) * a.Hq + hq) * a.Nq + i;
+      *reinterpret_cast<uint2 *>(a.O + at * D + c) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      // l is in units of 2^m: the sum of exp(score) is l 2^m
+      if (c == 0 && a.lse) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+    }
+  }
+  if (ranks > 1) cluster_sync();   // no CTA leaves while another reads it
+}
+
+}  // namespace mcs

@@ -1,0 +1,284 @@
+// kvcache_kernels.cuh -- the paged cache of keys and values held in e4m3, with
+// one scale per (page, head), for keys and for values: appending tokens (keys
+// rotated on the way) and reading them back as bf16.
+//
+// A stored number stands for e4m3 * scale.  append writes powers of two,
+// scale = 2^e with the smallest e in [-60, 60] whose 448 * 2^e holds the
+// page's largest finite magnitude.  With e4m3 (a floating format) a power of
+// two costs no precision against the exact ratio: the relative rounding is
+// 2^-4 at most for every number down to 2^-14 of the largest, e4m3's normal
+// range.  What it buys: when a later token of the page needs a larger scale,
+// the numbers already held move by a whole number of binades, exactly unless
+// they fall below e4m3's normal range (2^-6), and dequantising is exact in
+// bf16.  New numbers are rounded once, from the rotated fp32 value.
+//
+// Non-finite numbers: +-inf is held as the largest magnitude (+-448 * scale).
+// A token with a NaN among a head's key or value has its key there held as
+// NaN throughout and the value's NaN as 0: its score is then NaN in every row
+// that sees it, and rows that do not see it are not reached (a NaN held in V
+// would reach them as 0 * NaN).
+//
+// Both kernels are bound by memory (16 -> 8 bits per number, and back).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "rotary.cuh"
+
+namespace mcs {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int kScaleExp = 60;
+
+struct CacheView {
+  uint8_t *k, *v;                // e4m3 [n_pages, H, page, d]
+  float *k_scale, *v_scale;      // [n_pages, H]
+  const int32_t *table;          // [B, max_pages]
+  int n_pages, max_pages, H, page, d;
+};
+
+// two fp32 numbers to two e4m3 bytes (lo in the low byte), to nearest, +-inf and
+// what is out of range to +-448, NaN to NaN
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two e4m3 bytes to two halves (exact)
+__device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t lo16) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(lo16));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of_e4m3x2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ float2 float2_of_half2(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// the smallest 2^e, |e| <= 60, with amax <= 448 * 2^e (amax >= 0, finite)
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  // amax = 1.f * 2^x: 448 * 2^e = 1.75 * 2^(8 + e)
+  int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = min(max(e, -kScaleExp), kScaleExp);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float y = fabsf(x);
+  return y < __uint_as_float(0x7F800000u) ? y : 0.f;   // inf and NaN count as 0
+}
+
+struct AppendArgs {
+  CacheView c;
+  const bf16 *K, *V;
+  long long k_sb, k_sh, k_sn, v_sb, v_sh, v_sn;   // strides in numbers
+  const int32_t *start;                            // [B] first new token's place
+  const int32_t *counts;                           // [B] new tokens of each sequence, or null: n
+  const int32_t *pos;                              // [B, n, axes], or null: the token's place
+  long long pos_b, pos_n;
+  RotaryTable t;                                   // pairs == 0: no rotation
+  int n;
+  unsigned *status;
+};
+
+constexpr int kAppendThreads = 256;
+
+// One CTA per (page that may be touched, head, sequence): grid (pages, H, B).
+// U: units of 16 numbers per thread, ceil(page * d / 16 / 256).
+template <int U>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ unsigned s_amax[2];
+  __shared__ unsigned char s_nan[128];
+  const CacheView &c = a.c;
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+  const int start = a.start[b];
+  const int count = a.counts ? min(a.counts[b], a.n) : a.n;
+  if (count <= 0) return;
+  if (start < 0) {
+    if (tid == 0) record_status(a.status, kStatusBadMeta);
+    return;
+  }
+  const long long end = static_cast<long long>(start) + count;
+  const long long at = start / c.page + static_cast<long long>(blockIdx.x);   // the sequence's page
+  if (at * c.page >= end) return;
+  int pid = -1;
+  if (at < c.max_pages) pid = c.table[static_cast<long long>(b) * c.max_pages + at];
+  if (pid < 0 || pid >= c.n_pages) {   // behind the table, or no page of the pool: nothing is written
+    if (tid == 0) record_status(a.status, kStatusBadMeta);
+    return;
+  }
+  const int base = static_cast<int>(at * c.page);             // < max_pages * page < 2^31
+  const int lo = max(start - base, 0);                        // new slots [lo, hi)
+  const int hi = static_cast<int>(min(end - base, static_cast<long long>(c.page)));
+  const int upt = c.d / 16;                                   // units per token
+  const size_t row0 = (static_cast<size_t>(pid) * c.H + h) * c.page;
+  const size_t sidx = static_cast<size_t>(pid) * c.H + h;
+  if (tid < 2) s_amax[tid] = 0;
+  if (tid < 128) s_nan[tid] = 0;
+  __syncthreads();
+
+  float kx[U][8], ky[U][8], vx[U][8], vy[U][8];
+  float ak = 0.f, av = 0.f;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int id = tid + j * kAppendThreads, slot = lo + id / upt, u = id % upt;
+    if (slot < hi) {
+      const int i = base + slot - start;                      // the call's token
+      const RotUnit r = rotary_unit(a.t, u);
+      const bf16 *kp = a.K + b * a.k_sb + h * a.k_sh + i * a.k_sn;
+      const bf16 *vp = a.V + b * a.v_sb + h * a.v_sh + i * a.v_sn;
+      RotVec<bf16> w0, w1, w2, w3;
+      w0.load(kp + r.first);
+      w1.load(kp + r.second);
+      w2.load(vp + r.first);
+      w3.load(vp + r.second);
+      w0.get(kx[j]);
+      w1.get(ky[j]);
+      w2.get(vx[j]);
+      w3.get(vy[j]);
+      if (r.n_rot > 0) {
+        const int32_t place = base + slot;
+        float cs[8], sn[8];
+        rotary_unit_angles(a.t, r, a.pos ? a.pos + b * a.pos_b + i * a.pos_n : &place, cs, sn);
+        rotary_turn(a.t.interleaved, cs, sn, kx[j], ky[j]);
+      }
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ak = fmaxf(ak, fmaxf(finite_abs(kx[j][e]), finite_abs(ky[j][e])));
+        av = fmaxf(av, fmaxf(finite_abs(vx[j][e]), finite_abs(vy[j][e])));
+        bad |= isnan(kx[j][e]) || isnan(ky[j][e]) || isnan(vx[j][e]) || isnan(vy[j][e]);
+      }
+      if (bad) s_nan[slot] = 1;
+    }
+  }
+  // magnitudes order as their bits do
+  const unsigned mk = __reduce_max_sync(0xffffffffu, __float_as_uint(ak));
+  const unsigned mv = __reduce_max_sync(0xffffffffu, __float_as_uint(av));
+  if ((tid & 31) == 0) {
+    atomicMax(&s_amax[0], mk);
+    atomicMax(&s_amax[1], mv);
+  }
+  float ok = 0.f, ov = 0.f;                                   // the scales of the tokens held before
+  if (lo > 0) {
+    ok = c.k_scale[sidx];
+    ov = c.v_scale[sidx];
+  }
+  __syncthreads();
+  const float sk = fmaxf(e4m3_scale(__uint_as_float(s_amax[0])), ok);
+  const float sv = fmaxf(e4m3_scale(__uint_as_float(s_amax[1])), ov);
+  // tokens held before move to the larger scale (their slots are [0, lo))
+  for (int w = 0; w < 2; ++w) {
+    const float was = w ? ov : ok, now = w ? sv : sk;
+    if (lo > 0 && now > was) {
+      const float f = was / now;
+      uint4 *p = reinterpret_cast<uint4 *>((w ? c.v : c.k) + row0 * c.d);
+      for (int id = tid; id < lo * upt; id += kAppendThreads) {
+        uint4 q = p[id];
+        uint32_t *x = reinterpret_cast<uint32_t *>(&q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u0 = float2_of_half2(half2_of_e4m3x2(x[e])), u1 = float2_of_half2(half2_of_e4m3x2_hi(x[e]));
+          x[e] = e4m3x2(u0.x * f, u0.y * f) | e4m3x2(u1.x * f, u1.y * f) << 16;
+        }
+        p[id] = q;
+      }
+    }
+  }
+  const float ik = 1.f / sk, iv = 1.f / sv;                   // exact for powers of two
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int id = tid + j * kAppendThreads, slot = lo + id / upt, u = id % upt;
+    if (slot < hi) {
+      const RotUnit r = rotary_unit(a.t, u);
+      const bool bad = s_nan[slot] != 0;
+      auto pack = [&](const float (&x)[8], float f, bool value) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p = x[2 * e] * f, q = x[2 * e + 1] * f;
+          if (value) {   // a value's NaN is held as 0
+            p = isnan(p) ? 0.f : p;
+            q = isnan(q) ? 0.f : q;
+          }
+          w[e] = e4m3x2(p, q);
+        }
+        uint2 o = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        if (bad && !value) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        return o;
+      };
+      uint8_t *kp = c.k + (row0 + slot) * c.d, *vp = c.v + (row0 + slot) * c.d;
+      *reinterpret_cast<uint2 *>(kp + r.first) = pack(kx[j], ik, false);
+      *reinterpret_cast<uint2 *>(kp + r.second) = pack(ky[j], ik, false);
+      *reinterpret_cast<uint2 *>(vp + r.first) = pack(vx[j], iv, true);
+      *reinterpret_cast<uint2 *>(vp + r.second) = pack(vy[j], iv, true);
+    }
+  }
+  if (tid == 0) {
+    c.k_scale[sidx] = sk;
+    c.v_scale[sidx] = sv;
+  }
+}
+
+struct ReadArgs {
+  CacheView c;
+  const int32_t *start, *counts;   // [B]; counts may be null: n
+  bf16 *K, *V;                     // [B, H, n, d]
+  int n;
+  long long units;                 // B * H * n * d / 16
+  unsigned *status;
+};
+
+constexpr int kReadThreads = 256;
+
+// One thread per 16 numbers of a token and head, of K and of V.
+__global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+  const CacheView &c = a.c;
+  const long long id = static_cast<long long>(blockIdx.x) * kReadThreads + threadIdx.x;
+  if (id >= a.units) return;
+  const int upt = c.d / 16;
+  const long long row = id / upt;                       // (b, h, i)
+  const int u = static_cast<int>(id - row * upt);
+  const long long bh = row / a.n;
+  const int i = static_cast<int>(row - bh * a.n);
+  const int b = static_cast<int>(bh / c.H), h = static_cast<int>(bh - static_cast<long long>(b) * c.H);
+  const long long pos = static_cast<long long>(a.start[b]) + i;
+  const long long at = pos / c.page;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  float sk = 0.f, sv = 0.f;
+  if (pos >= 0 && at < c.max_pages && (!a.counts || i < a.counts[b])) {
+    const int pid = c.table[static_cast<long long>(b) * c.max_pages + at];
+    if (pid >= 0 && pid < c.n_pages) {
+      const size_t s = static_cast<size_t>(pid) * c.H + h;
+      const size_t off = (s * c.page + static_cast<size_t>(pos - at * c.page)) * c.d + 16 * u;
+      k = *reinterpret_cast<const uint4 *>(c.k + off);
+      v = *reinterpret_cast<const uint4 *>(c.v + off);
+      sk = c.k_scale[s];
+      sv = c.v_scale[s];
+    } else {
+      record_status(a.status, kStatusBadMeta);
+    }
+  }
+  auto put = [&](bf16 *out, const uint4 &q, float s) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 lo = float2_of_half2(half2_of_e4m3x2(w[e])), hi = float2_of_half2(half2_of_e4m3x2_hi(w[e]));
+      o[2 * e] = pack_bf16x2(lo.x * s, lo.y * s);
+      o[2 * e + 1] = pack_bf16x2(hi.x * s, hi.y * s);
+    }
+    uint4 *p = reinterpret_cast<uint4 *>(out + row * c.d + 16 * u);
+    p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  };
+  put(a.K, k, sk);
+  put(a.V, v, sv);
+}
+
+}  // namespace mcs

@@ -14,6 +14,7 @@
 #include "attn_kernel.cuh"
 #include "colsum_kernel.cuh"
 #include "group_kernels.cuh"
+#include "host_shared.h"
 #include "pair_kernel.cuh"
 #include "residual_compact.cuh"
 #include "topk_kernel.cuh"
@@ -101,6 +102,29 @@ bool map_tile(CUtensorMap *m, const void *base, int D, int N, int BH) {
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+namespace mcs {
+
+unsigned *device_status_word() { return status_ptr(); }
+uint64_t wait_limit_ns() { return g_wait_ns; }
+
+bool map_byte_rows(CUtensorMap *m, const void *base, int row_bytes, size_t rows, unsigned box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mcs
+
+namespace {
 
 // SMs of the current device
 cudaError_t sm_count(int *n) {

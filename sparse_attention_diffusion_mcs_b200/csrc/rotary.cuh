@@ -1,0 +1,268 @@
+// rotary.cuh -- rotary positions: each pair (a, b) of a head's numbers is
+// turned by the angle t = pos * f of its pair,
+//   a' = mag (a cos t - b sin t),   b' = mag (a sin t + b cos t),
+// and the gradient is the same map with -t.
+//
+// Angles: f is held as the 64-bit fraction of a turn F = round(f / 2pi * 2^64).
+// pos * F mod 2^64 is then the phase, exact for every 32-bit position (the
+// product wraps whole turns away; F's own rounding moves it by less than
+// pos * 2^-65 turns), so far positions lose nothing and no table of angles is
+// read.  The phase's top 32 bits, as a signed number of half turns, go to
+// sincospif: its rounding to fp32 costs at most 2^-25 half turns (9.4e-8 rad).
+//
+// The kernel is bound by memory: every number is read and written once.  A
+// thread owns 16 numbers of one token (8 pairs, two 16-byte vectors for 16-bit
+// types) and walks over the heads, so the angles are computed once for all
+// heads of its group.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "mcs_common.cuh"
+
+namespace mcs {
+
+struct RotaryTable {
+  const unsigned long long *turns;   // [pairs] fractions of a turn per position, times 2^64
+  const int32_t *axis;               // [pairs] position axis each pair goes by
+  int pairs;                         // rotated pairs of a head (may be 0)
+  int interleaved;                   // pairs (2i, 2i+1) instead of (i, pairs + i)
+  int axes;                          // numbers per position
+  float mag;                         // factor on the rotated numbers
+};
+
+// cos and sin of pair i at the position whose axis numbers are at `pos`
+__device__ __forceinline__ void rotary_angle(const RotaryTable &t, int i, const int32_t *pos, float &c, float &s) {
+  const unsigned long long f = t.turns[i];
+  const long long p = pos[t.axis[i]];
+  const int32_t phase = static_cast<int32_t>((static_cast<unsigned long long>(p) * f) >> 32);
+  sincospif(static_cast<float>(phase) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+}
+
+template <typename T>
+struct RotVec;   // 8 numbers
+template <>
+struct RotVec<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = *reinterpret_cast<const float4 *>(p);
+    b = *reinterpret_cast<const float4 *>(p + 4);
+  }
+  __device__ __forceinline__ void store(float *p) const {
+    *reinterpret_cast<float4 *>(p) = a;
+    *reinterpret_cast<float4 *>(p + 4) = b;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+template <>
+struct RotVec<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = u; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+  }
+};
+template <>
+struct RotVec<__half> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __half *p) { u = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void store(__half *p) const { *reinterpret_cast<uint4 *>(p) = u; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+__device__ __forceinline__ float rot_get(float x) { return x; }
+__device__ __forceinline__ float rot_get(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float rot_get(__half x) { return __half2float(x); }
+__device__ __forceinline__ void rot_put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void rot_put(bf16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void rot_put(__half *p, float x) { *p = __float2half_rn(x); }
+
+// Where unit u of a head (16 numbers) lies: its two 8-number vectors start at
+// first and second; n_rot of its pairs turn, the first being pair `pair`.
+// Half layout: vector `first` holds the pairs' a, `second` their b (or, behind
+// the rotated part, 16 numbers that stay).  Interleaved: 16 numbers in a row.
+// The half layout needs pairs % 8 == 0.
+struct RotUnit {
+  int first, second, pair, n_rot;
+};
+__device__ __forceinline__ RotUnit rotary_unit(const RotaryTable &t, int u) {
+  RotUnit r;
+  if (t.interleaved) {
+    r.first = 16 * u;
+    r.second = r.first + 8;
+    r.pair = 8 * u;
+    r.n_rot = min(max(t.pairs - r.pair, 0), 8);
+  } else if (8 * u < t.pairs) {
+    r.first = 8 * u;
+    r.second = t.pairs + 8 * u;
+    r.pair = 8 * u;
+    r.n_rot = 8;
+  } else {
+    r.first = 2 * t.pairs + 16 * (u - t.pairs / 8);
+    r.second = r.first + 8;
+    r.pair = 0;
+    r.n_rot = 0;
+  }
+  return r;
+}
+
+// cos and sin (times mag) of the unit's pairs; (1, 0) for pairs that stay
+__device__ __forceinline__ void rotary_unit_angles(const RotaryTable &t, const RotUnit &r, const int32_t *pos,
+                                                   float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = 1.f;
+    s[i] = 0.f;
+    if (i < r.n_rot) {
+      rotary_angle(t, r.pair + i, pos, c[i], s[i]);
+      c[i] *= t.mag;
+      s[i] *= t.mag;
+    }
+  }
+}
+
+// the unit's 16 numbers turned in place: x its first vector, y its second
+__device__ __forceinline__ void rotary_turn(bool interleaved, const float (&c)[8], const float (&s)[8], float (&x)[8],
+                                            float (&y)[8]) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = fmaf(a, c[i], -b * s[i]);
+      x[2 * i + 1] = fmaf(a, s[i], b * c[i]);
+      const float e = y[2 * i], f = y[2 * i + 1];
+      y[2 * i] = fmaf(e, c[4 + i], -f * s[4 + i]);
+      y[2 * i + 1] = fmaf(e, s[4 + i], f * c[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[i], b = y[i];
+      x[i] = fmaf(a, c[i], -b * s[i]);
+      y[i] = fmaf(a, s[i], b * c[i]);
+    }
+  }
+}
+
+struct RotateArgs {
+  const void *x;
+  void *out;                         // contiguous [B, H, N, d]
+  const int32_t *pos;                // [B, N, axes], strides pos_b and pos_n
+  long long sb, sh, sn;              // strides of x in numbers (d's is 1)
+  long long pos_b, pos_n;
+  RotaryTable t;
+  int B, H, N, d;
+  int heads;                         // heads per group: blockIdx.y takes [y * heads, ...)
+  int back;                          // turn by -t (the gradient)
+};
+
+constexpr int kRotateThreads = 256;
+
+// VEC: 16-byte vectors (see the host's rule); else one pair per thread, for
+// any strides, alignment and number of pairs.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+  const int per_token = VEC ? a.d / 16 : a.d - a.t.pairs;   // units, or pairs and single numbers behind them
+  const long long id = static_cast<long long>(blockIdx.x) * kRotateThreads + threadIdx.x;
+  const long long token = id / per_token;
+  if (token >= static_cast<long long>(a.B) * a.N) return;
+  const int u = static_cast<int>(id - token * per_token);
+  const int b = static_cast<int>(token / a.N), n = static_cast<int>(token - static_cast<long long>(b) * a.N);
+  const int32_t *pos = a.pos + b * a.pos_b + n * a.pos_n;
+  const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.H);
+  const T *src = static_cast<const T *>(a.x) + b * a.sb + n * a.sn;
+  T *dst = static_cast<T *>(a.out) + (static_cast<size_t>(b) * a.H * a.N + n) * a.d;
+  const size_t dst_h = static_cast<size_t>(a.N) * a.d;
+  if constexpr (VEC) {
+    const RotUnit r = rotary_unit(a.t, u);
+    float c[8], s[8];
+    rotary_unit_angles(a.t, r, pos, c, s);
+    if (a.back) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = -s[i];
+    }
+    auto turn = [&](RotVec<T> &vx, RotVec<T> &vy) {
+      float x[8], y[8];
+      vx.get(x);
+      vy.get(y);
+      rotary_turn(a.t.interleaved || r.n_rot == 0, c, s, x, y);
+      vx.set(x);
+      vy.set(y);
+    };
+    constexpr int U = sizeof(T) == 4 ? 2 : 4;   // heads in flight
+    int h = h0;
+    for (; h + U <= h1; h += U) {
+      RotVec<T> vx[U], vy[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        vx[i].load(src + (h + i) * a.sh + r.first);
+        vy[i].load(src + (h + i) * a.sh + r.second);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        turn(vx[i], vy[i]);
+        vx[i].store(dst + (h + i) * dst_h + r.first);
+        vy[i].store(dst + (h + i) * dst_h + r.second);
+      }
+    }
+    for (; h < h1; ++h) {
+      RotVec<T> vx, vy;
+      vx.load(src + h * a.sh + r.first);
+      vy.load(src + h * a.sh + r.second);
+      turn(vx, vy);
+      vx.store(dst + h * dst_h + r.first);
+      vy.store(dst + h * dst_h + r.second);
+    }
+  } else {
+    if (u < a.t.pairs) {
+      const int first = a.t.interleaved ? 2 * u : u, second = a.t.interleaved ? 2 * u + 1 : a.t.pairs + u;
+      float c, s;
+      rotary_angle(a.t, u, pos, c, s);
+      c *= a.t.mag;
+      s *= a.back ? -a.t.mag : a.t.mag;
+      for (int h = h0; h < h1; ++h) {
+        const float x = rot_get(src[h * a.sh + first]), y = rot_get(src[h * a.sh + second]);
+        rot_put(dst + h * dst_h + first, fmaf(x, c, -y * s));
+        rot_put(dst + h * dst_h + second, fmaf(x, s, y * c));
+      }
+    } else {
+      const int e = a.t.pairs + u;
+      for (int h = h0; h < h1; ++h) dst[h * dst_h + e] = src[h * a.sh + e];
+    }
+  }
+}
+
+}  // namespace mcs
