@@ -461,11 +461,16 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
  * lse: float32 [B, Hq, Nq] or NULL: log of the sum of exp of a row's scores.
  * A row that sees nothing gives zeros, and -inf in lse.  Weights and products:
  * fp32 sums and statistics of exact 8-bit numbers and 16-bit weights.
- * Nq == 0 is a no-op.  Needs no workspace; repeats bit for bit.  Asynchronous.
+ * workspace: 16-byte aligned device memory of the size that the first function
+ *   gives for the same arguments on the current device (0: none needed), this
+ *   call's own until it has run on its stream; nothing in it matters before or
+ *   after.
+ * Nq == 0 is a no-op.  Repeats bit for bit.  Asynchronous.
  */
+size_t mcs_cache_attention_workspace_size(const mcs_cache *cache, int Hq, int Nq);
 mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, int Nq, const int32_t *lengths,
-                               const int32_t *counts, int causal, float scale, void *O, float *lse,
-                               mcs_stream_t stream);
+                               const int32_t *counts, int causal, float scale, void *O, float *lse, void *workspace,
+                               size_t workspace_bytes, mcs_stream_t stream);
 
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns MCS_OK, or MCS_ERR_TIMEOUT if a kernel's bounded wait ran out

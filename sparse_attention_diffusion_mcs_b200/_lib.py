@@ -87,7 +87,9 @@ PROTOTYPES = {
     "mcs_cache_append": (c_int, [PCACHE, c_vp, c_vp, PI64, PI64, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, PROTARY,
                                  c_vp]),
     "mcs_cache_read": (c_int, [PCACHE, c_vp, c_vp, c_int, c_vp, c_vp, c_vp]),
-    "mcs_cache_attention": (c_int, [PCACHE, c_vp, c_int, c_int, c_vp, c_vp, c_int, c_float, c_vp, c_vp, c_vp]),
+    "mcs_cache_attention_workspace_size": (c_size_t, [PCACHE, c_int, c_int]),
+    "mcs_cache_attention": (c_int, [PCACHE, c_vp, c_int, c_int, c_vp, c_vp, c_int, c_float, c_vp, c_vp, c_vp, c_size_t,
+                                    c_vp]),
     "mcs_last_device_status": (c_int, [c_vp]),
     "mcs_selftest_wait_timeout": (c_int, [c_u64, c_vp]),
     "mcs_set_wait_limit_ns": (None, [c_u64]),

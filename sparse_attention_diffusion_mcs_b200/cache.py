@@ -179,7 +179,10 @@ def cache_attention(Q: torch.Tensor, cache: KVCache, lengths: torch.Tensor, caus
         api._check_tensor(out, "out", Q.shape, torch.bfloat16, cache.device)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=cache.device) if return_lse else None
     with api._on(cache.device):
+        need = lib().mcs_cache_attention_workspace_size(ctypes.byref(cache._c), Hq, Nq)
+        ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
         check(lib().mcs_cache_attention(ctypes.byref(cache._c), Q.data_ptr(), Hq, Nq, kept, how_many, int(causal),
                                         api._scale(d, scale), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                                        api._stream(cache.device)), "mcs_cache_attention")
+                                        0 if ws is None else ws.data_ptr(), need, api._stream(cache.device)),
+              "mcs_cache_attention")
     return (out, lse) if return_lse else out

@@ -112,37 +112,82 @@ cudaError_t launch_rotate(RotateArgs &a, bool vec, const Device &dev, cudaStream
 }
 
 // ---------------------------------------------------------------- attention over the cache
+// CTAs that deal the work of one call among themselves, at most (two on each SM)
+constexpr int kMaxCtas = 2 * 148;
+
+// sizes of one call: blocks of rows, and how they are computed
+struct AttnPlan {
+  int mt;                        // row tiles of 16 of a block (cache_rows_kernel)
+  int rows;                      // rows of a block
+  int ctas;                      // CTAs that share the work; 0: clusters, no workspace
+  int split;                     // CTAs of a cluster
+};
+AttnPlan plan_attention(const CacheView &c, int B, long long n_rows, int sms) {
+  AttnPlan p;
+  p.mt = n_rows <= 16 ? 1 : 2;
+  p.rows = 16 * p.mt;
+  const long long blocks = (n_rows + p.rows - 1) / p.rows;
+  const long long items = static_cast<long long>(B) * c.H * blocks;
+  const long long tiles = (static_cast<long long>(c.max_pages) * c.page + kKeyTile - 1) / kKeyTile;
+  const int resident = sms * (p.mt == 1 ? 2 : 1);
+  p.ctas = resident < kMaxCtas ? resident : kMaxCtas;
+  p.split = 1;
+  // Little work (by the table's places; lengths are not known here): clusters
+  // of 8 CTAs (the portable size) at most, as many as fill the SMs once and as
+  // there can be tiles.
+  if (blocks <= 65535 && tiles <= 64 && items * tiles <= 16ll * sms) {
+    long long split = resident / items;
+    split = split > 8 ? 8 : split;
+    split = split > tiles ? tiles : split;
+    p.split = static_cast<int>(split < 1 ? 1 : split);
+    p.ctas = 0;
+  }
+  return p;
+}
+
 template <int D, int MT>
-cudaError_t launch_rows(CacheAttnArgs &a, const Device &dev, cudaStream_t s) {
+cudaError_t launch_rows(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, cudaStream_t s) {
   using C = RowsCfg<D, MT>;
-  static_assert(C::SMEM * (MT == 1 ? 2 : 1) <= 232448, "shared memory budget");
-  cudaError_t e = allow_smem<cache_rows_kernel<D, MT>>(dev, C::SMEM);
+  static_assert(C::SMEM * (MT == 1 ? 2 : 1) + (MT == 1 ? 2048 : 0) <= 232448, "shared memory budget");
+  if (p.ctas) {
+    cudaError_t e = allow_smem<cache_rows_kernel<D, MT, false>>(dev, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cache_rows_kernel<D, MT, false><<<p.ctas, C::THREADS, C::SMEM, s>>>(a);
+    return cudaGetLastError();
+  }
+  cudaError_t e = allow_smem<cache_rows_kernel<D, MT, true>>(dev, C::SMEM);
   if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(a.Nq) * a.share;
-  const long long blocks = (rows + 16 * MT - 1) / (16 * MT);
-  if (blocks > 65535) return cudaErrorInvalidValue;
-  // One cluster per (sequence, key head, block of rows), its CTAs sharing the
-  // key tiles: as many as fill the SMs once, 8 (the portable size) at most,
-  // and no more than there can be tiles.
-  const long long items = static_cast<long long>(a.B) * a.c.H * blocks;
-  const long long tiles = (static_cast<long long>(a.c.max_pages) * a.c.page + C::BN - 1) / C::BN;
-  long long split = static_cast<long long>(dev.sms) * (MT == 1 ? 2 : 1) / items;
-  split = split > 8 ? 8 : split;
-  split = split > tiles ? tiles : split;
-  split = split < 1 ? 1 : split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(split), static_cast<unsigned>(a.B * a.c.H), static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.split), static_cast<unsigned>(a.s.B * a.s.H),
+                     static_cast<unsigned>(a.s.n_blocks));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = static_cast<unsigned>(split);
+  at.val.clusterDim.x = static_cast<unsigned>(p.split);
   at.val.clusterDim.y = 1;
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<D, MT>, a);
+  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<D, MT, true>, a);
+}
+
+template <int D>
+cudaError_t launch_merge(const CacheAttnArgs &a, const AttnPlan &p, cudaStream_t s) {
+  MergeArgs m;
+  std::memset(&m, 0, sizeof(m));
+  m.m = a.m;
+  m.O = a.O;
+  m.lse = a.lse;
+  m.H = a.s.H;
+  m.Nq = a.s.Nq;
+  m.share = a.s.share;
+  m.n_rows = a.s.n_rows;
+  m.rows = p.rows;
+  const int at_once = kMergeThreads / (D / 4);
+  cache_merge_kernel<D><<<dim3(p.ctas, (p.rows + at_once - 1) / at_once), kMergeThreads, 0, s>>>(m);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -261,9 +306,19 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
   return cuda_status(cudaGetLastError());
 }
 
+size_t mcs_cache_attention_workspace_size(const mcs_cache *cache, int Hq, int Nq) {
+  CacheView c;
+  Device dev;
+  if (check_cache(cache, &c) != MCS_OK || Hq < 1 || Hq % c.H != 0 || Nq < 0) return 0;
+  const long long n_rows = static_cast<long long>(Nq) * (Hq / c.H);
+  if (n_rows == 0 || n_rows > (1 << 20) || !current_device(&dev)) return 0;
+  const AttnPlan p = plan_attention(c, cache->B, n_rows, dev.sms);
+  return p.ctas ? merge_space(p.ctas, p.rows, c.d, nullptr, nullptr) : 0;
+}
+
 mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, int Nq, const int32_t *lengths,
-                               const int32_t *counts, int causal, float scale, void *O, float *lse,
-                               mcs_stream_t stream) {
+                               const int32_t *counts, int causal, float scale, void *O, float *lse, void *workspace,
+                               size_t workspace_bytes, mcs_stream_t stream) {
   CacheAttnArgs a;
   std::memset(&a, 0, sizeof(a));
   const mcs_status st = check_cache(cache, &a.c);
@@ -273,30 +328,40 @@ mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, in
   if (Nq == 0) return MCS_OK;
   if (!Q || !O || !lengths || !aligned16(Q) || !aligned16(O) || !aligned4(lengths) || !aligned4(counts) || !aligned4(lse))
     return MCS_ERR_INVALID_ARG;
-  if (static_cast<long long>(Nq) * (Hq / a.c.H) > (1 << 20)) return MCS_ERR_INVALID_ARG;
+  const long long n_rows = static_cast<long long>(Nq) * (Hq / a.c.H);
+  if (n_rows > (1 << 20)) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return MCS_ERR_INVALID_ARG;
+  Device dev;
+  if (!current_device(&dev) || !(a.status = device_status_word())) return MCS_ERR_CUDA;
+  const AttnPlan p = plan_attention(a.c, cache->B, n_rows, dev.sms);
+  if (p.ctas) {
+    if (!workspace || workspace_bytes < merge_space(p.ctas, p.rows, a.c.d, nullptr, nullptr)) return MCS_ERR_WORKSPACE;
+    merge_space(p.ctas, p.rows, a.c.d, workspace, &a.m);
+  }
   a.Q = static_cast<const bf16 *>(Q);
   a.O = static_cast<bf16 *>(O);
   a.lse = lse;
-  a.lengths = lengths;
-  a.counts = counts;
-  a.B = cache->B;
-  a.Hq = Hq;
-  a.Nq = Nq;
-  a.share = Hq / a.c.H;
-  a.causal = causal != 0;
+  a.s.lengths = lengths;
+  a.s.counts = counts;
+  a.s.B = cache->B;
+  a.s.H = a.c.H;
+  a.s.Nq = Nq;
+  a.s.share = Hq / a.c.H;
+  a.s.causal = causal != 0;
+  a.s.cap = a.c.max_pages * a.c.page;
+  a.s.n_rows = static_cast<int>(n_rows);
+  a.s.n_blocks = static_cast<int>((n_rows + p.rows - 1) / p.rows);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = wait_limit_ns();
-  Device dev;
-  if (!current_device(&dev) || !(a.status = device_status_word())) return MCS_ERR_CUDA;
   const size_t rows = static_cast<size_t>(a.c.n_pages) * a.c.H * a.c.page;
   if (!map_byte_rows(&a.tmK, a.c.k, a.c.d, rows, a.c.page) || !map_byte_rows(&a.tmV, a.c.v, a.c.d, rows, a.c.page))
     return MCS_ERR_CUDA;
-  const bool one = static_cast<long long>(Nq) * a.share <= 16;
   cudaError_t e;
   if (a.c.d == 64)
-    e = one ? launch_rows<64, 1>(a, dev, cu(stream)) : launch_rows<64, 2>(a, dev, cu(stream));
+    e = p.mt == 1 ? launch_rows<64, 1>(a, p, dev, cu(stream)) : launch_rows<64, 2>(a, p, dev, cu(stream));
   else
-    e = one ? launch_rows<128, 1>(a, dev, cu(stream)) : launch_rows<128, 2>(a, dev, cu(stream));
+    e = p.mt == 1 ? launch_rows<128, 1>(a, p, dev, cu(stream)) : launch_rows<128, 2>(a, p, dev, cu(stream));
+  if (e == cudaSuccess && p.ctas) e = a.c.d == 64 ? launch_merge<64>(a, p, cu(stream)) : launch_merge<128>(a, p, cu(stream));
   return cuda_status(e);
 }
 

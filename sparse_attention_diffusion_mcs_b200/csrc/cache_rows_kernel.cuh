@@ -7,17 +7,21 @@
 // m_i the running maximum of y.  2^y = 2^x vs is the weight that v8 itself
 // gets, so the held numbers enter the products as they are (e4m3 is exact in
 // fp16), every weight is <= 1 whatever the pages' scales, and no page is
-// dequantised.  m, the sums and O are fp32; the weights are rounded to fp16
-// (2^-11 relative; below 2^-14 of the row's largest weight, an absolute 2^-25).
+// dequantised.  m, the sums and O are fp32; the weights, times 2^14, are
+// rounded to fp16 (2^-11 relative; below 2^-28 of the row's largest weight, an
+// absolute 2^-39 of it).
 // Queries are held as fp16 of q 2^-e, 2^e the power of two at the row's
 // largest magnitude: exact for bf16 numbers down to 2^-17 of it, and off by
 // 2^-25 of it below.
 //
 // A CTA takes 16 MT rows -- all query heads that share a key head, times their
-// tokens -- and a run of 128-key tiles; a cluster of C CTAs takes a whole
-// sequence, each CTA its share of the tiles, and merges (m, l, O) through
-// distributed shared memory: no workspace and no second launch, and the merge
-// order is fixed, so results repeat bit for bit.
+// tokens -- and runs of 128-key tiles, dealt in one of two ways.  Little work:
+// a cluster of CTAs takes one item (cache_sched.cuh), each its share of the
+// tiles, and merges (m, l, O) through distributed shared memory, in one launch.
+// Much work: the CTAs that fill the SMs once take equal runs of all items'
+// tiles, and a second launch merges what was split; sequences of any lengths
+// then keep every SM reading to the end.  Either way the merge order is fixed,
+// so results repeat bit for bit.
 // Products by mma.sync m16n8k16: one row tile of 16 is all there is, while a
 // tcgen05 product has at least 64 rows, needs its operands in 16 bits in
 // shared memory (an extra write and read of every number), and 16 rows
@@ -30,7 +34,7 @@
 // memory read free of bank conflicts (key_of below).
 #pragma once
 
-#include "kvcache_kernels.cuh"
+#include "cache_sched.cuh"
 
 namespace mcs {
 
@@ -40,10 +44,8 @@ struct CacheAttnArgs {
   const bf16 *Q;                 // [B, Hq, Nq, d]
   bf16 *O;                       // [B, Hq, Nq, d]
   float *lse;                    // [B, Hq, Nq] or null: log of the sum of exp (natural units)
-  const int32_t *lengths;        // [B] tokens kept
-  const int32_t *counts;         // [B] query tokens, or null: Nq
-  int B, Hq, Nq, share;          // share = Hq / H
-  int causal;
+  SchedArgs s;
+  MergeSpace m;                  // (not used by clusters)
   float scale_log2;
   unsigned *status;
   unsigned long long wait_ns;
@@ -57,15 +59,17 @@ struct RowsCfg {
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_SC = OFF_KV + NS * 2 * TILE;   // per stage: 8 x float4 (ks, log2 vs, 1 / vs, -)
   static constexpr int OFF_BAR = OFF_SC + NS * 8 * 16;
-  static constexpr int OFF_ML = OFF_BAR + 16 * NS;        // merged (m, l) of 16 MT rows
-  static constexpr int OFF_WML = OFF_ML + 16 * MT * 8;    // per warp (m, l)
-  static constexpr int OFF_MISC = OFF_WML + 4 * 16 * MT * 8;
-  static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  // after the last tile, over the ring: the warps' O, then the CTA's merged O
-  static constexpr int OLD = D + 4;
-  static constexpr int OFF_WO = 0;
-  static constexpr int OFF_O = OFF_WO + 4 * 16 * MT * OLD * 4;
-  static_assert(OFF_O + 16 * MT * D * 4 <= OFF_SC, "the merge fits the ring");
+  static constexpr int OFF_MISC = OFF_BAR + 16 * NS;
+  static constexpr int OFF_ML = OFF_MISC + 16;            // merged (reference, l) of 16 MT rows
+  static constexpr int OFF_WML = OFF_ML + 16 * MT * 8;    // per warp (reference, l)
+  // the warps' O on its way into the CTA's, 32 numbers of a row at a time
+  static constexpr int OLD = 32 + 4;
+  static constexpr int OFF_WO = OFF_WML + 4 * 16 * MT * 8;
+  static constexpr int SMEM = OFF_WO + 4 * 16 * MT * OLD * 4 + 1024;
+  // clusters, after their only run of tiles, over the ring: the CTA's O
+  static constexpr int OFF_O = 0;
+  static_assert(OFF_WML % 16 == 0 && OFF_WO % 16 == 0, "16-byte aligned");
+  static_assert(16 * MT * D * 4 <= OFF_SC, "a cluster's O fits the ring");
   static constexpr int THREADS = 5 * 32;
 };
 
@@ -111,14 +115,28 @@ __device__ __forceinline__ float4 ld_dsmem4(uint32_t addr, uint32_t rank) {
                : "memory");
   return v;
 }
+// a barrier of warps 0-3 that tells whether all of them are well
+__device__ __forceinline__ bool group_ok(bool ok) {
+  uint32_t bad;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(bad)
+      : "r"(ok ? 0u : 1u)
+      : "memory");
+  return bad == 0;
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int D, int MT>
+// weights are held times 2^kBias in fp16
+constexpr float kRowsBias = 14.f;
+
+template <int D, int MT, bool CLUSTER>
 __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     cache_rows_kernel(const __grid_constant__ CacheAttnArgs a) {
   using C = RowsCfg<D, MT>;
+  using S = Sched<16 * MT, false>;
   constexpr int NS = C::NS, BN = C::BN, SEG = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -130,32 +148,10 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
 
   const CacheView &cv = a.c;
+  const SchedArgs &sa = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x, ranks = gridDim.x;        // the cluster spans the x dimension
-  const int b = blockIdx.y / cv.H, h = blockIdx.y - b * cv.H;
-  const int row0 = blockIdx.z * 16 * MT;                 // rows are (token, query head of the group)
-  const int n_rows = a.Nq * a.share;
-  const long long cap = static_cast<long long>(cv.max_pages) * cv.page;
-  int len = a.lengths[b];
-  if (len > cap) {
-    if (tid == 0) record_status(a.status, kStatusBadMeta);
-    len = static_cast<int>(cap);
-  }
-  len = max(len, 0);
-  const int nq = a.counts ? min(max(a.counts[b], 0), a.Nq) : a.Nq;
-  // keys that row i of the sequence sees: [0, limit)
-  auto limit_of = [&](int row) {
-    const int i = row / a.share;
-    if (row >= n_rows || i >= nq) return 0;
-    return a.causal ? max(len - nq + i + 1, 0) : len;
-  };
-  const int last_row = min(row0 + 16 * MT, n_rows) - 1;
-  const int last_query = min(last_row, nq * a.share - 1);
-  const int kmax = last_query < row0 ? 0 : limit_of(last_query);   // later rows see no less
-  const int tiles = (kmax + BN - 1) / BN;
-  const int t0 = static_cast<int>(static_cast<long long>(tiles) * rank / ranks);
-  const int t1 = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / ranks);
-
+  const int rank = blockIdx.x, ranks = gridDim.x;        // CLUSTER: it spans the x dimension
+  const int share = sa.share;
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(b_full(s), 1);
@@ -164,8 +160,39 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  // every warp goes through the same parts
+  S run;
+  if constexpr (CLUSTER) {
+    run.b = blockIdx.y / sa.H;
+    run.h = blockIdx.y - run.b * sa.H;
+    run.block = blockIdx.z;
+    run.left = 1;
+    if (tid == 0 && sa.lengths[run.b] > sa.cap) record_status(a.status, kStatusBadMeta);
+  } else {
+    run.start(sa, rank, ranks, 4, lane, a.status);
+    if (tid == 0) a.m.items[rank].go_on = 0;
+  }
+  auto next = [&](Segment &g) -> bool {
+    if constexpr (CLUSTER) {
+      if (!run.left) return false;
+      run.left = 0;
+      g.b = run.b;
+      g.h = run.h;
+      g.block = run.block;
+      S::item(sa, g.b, g.block, g);
+      const int tiles = (g.kmax + BN - 1) / BN;
+      g.t0 = static_cast<int>(static_cast<long long>(tiles) * rank / ranks);
+      g.t1 = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / ranks);
+      return true;
+    } else {
+      if (!run.next(sa, g)) return false;
+      g.t1 = min(g.t1, (g.kmax + BN - 1) / BN);          // an item without keys has no tile to read
+      return true;
+    }
+  };
   __syncthreads();
 
+  Segment sg;
   if (warp == 4) {
     // ------------------------------------------------------------------ loads
     // lane l holds page and scales of the 16-key group 32 bt + l of batch bt
@@ -174,68 +201,69 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
       tma_prefetch_desc(&a.tmK);
       tma_prefetch_desc(&a.tmV);
     }
-    const int32_t *table = cv.table + static_cast<long long>(b) * cv.max_pages;
-    const int groups = (kmax + 15) / 16;
-    auto fetch_page = [&](int g) {
-      int p = -1;
-      if (g < groups) {
-        p = table[g * 16 / cv.page];
-        if (p < 0 || p >= cv.n_pages) {
-          record_status(a.status, kStatusBadMeta);
-          p = -1;
-        }
-      }
-      return p;
-    };
-    int pid = fetch_page(8 * t0 + lane);
-    float ks = 0.f, vs = 0.f;
-    auto fetch_scales = [&](int p, float &k, float &v) {
-      k = v = 0.f;
-      if (p >= 0) {
-        k = cv.k_scale[static_cast<size_t>(p) * cv.H + h];
-        v = cv.v_scale[static_cast<size_t>(p) * cv.H + h];
-      }
-    };
-    fetch_scales(pid, ks, vs);
     bool ok = true;
-    int issued = 0;
-    const int gpb = cv.page / 16;                    // groups per page (a page is at most a tile)
-    for (int tb = t0; tb < t1 && ok; tb += 4) {
-      const int npid = fetch_page(8 * (tb + 4) + lane);
-      float nks, nvs;
-      fetch_scales(npid, nks, nvs);
-      for (int t = tb; t < min(tb + 4, t1); ++t) {
-        const int it = t - t0, s = it % NS;
-        const int gl = 8 * (t - tb);                 // lane of the tile's first group
-        ok = mbar_wait_warp(b_empty(s), ((it / NS) & 1) ^ 1, a.wait_ns, abort_flag);
-        if (!ok) break;
-        if (lane >= gl && lane < gl + 8) {
-          float4 f;
-          f.x = ks;
-          f.y = pid >= 0 ? __log2f(vs) : -INFINITY;
-          f.z = pid >= 0 ? 1.f / vs : 0.f;
-          f.w = 0.f;
-          *reinterpret_cast<float4 *>(smem + C::OFF_SC + (s * 8 + lane - gl) * 16) = f;
+    int it = 0;                                      // tiles so far, over all parts
+    while (ok && next(sg)) {
+      const int32_t *table = cv.table + static_cast<long long>(sg.b) * cv.max_pages;
+      const int groups = (sg.kmax + 15) / 16;
+      auto fetch_page = [&](int g) {
+        int p = -1;
+        if (g < groups) {
+          p = table[g * 16 / cv.page];
+          if (p < 0 || p >= cv.n_pages) {
+            record_status(a.status, kStatusBadMeta);
+            p = -1;
+          }
         }
-        // the first lane of each page's groups loads it
-        const bool mine = lane >= gl && lane < gl + 8 && (lane - gl) % gpb == 0 && pid >= 0;
-        const unsigned who = __ballot_sync(0xffffffffu, mine);
-        const uint32_t page_bytes = static_cast<uint32_t>(cv.page) * D;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(b_full(s), __popc(who) * 2 * page_bytes);
-        __syncwarp();
-        if (mine) {
-          const uint32_t dst = sbase + C::OFF_KV + s * 2 * C::TILE + (lane - gl) * 16 * D;
-          const int r = static_cast<int>((static_cast<long long>(pid) * cv.H + h) * cv.page);
-          tma_load_2d(dst, &a.tmK, 0, r, b_full(s));
-          tma_load_2d(dst + C::TILE, &a.tmV, 0, r, b_full(s));
+        return p;
+      };
+      int pid = fetch_page(8 * sg.t0 + lane);
+      float ks = 0.f, vs = 0.f;
+      auto fetch_scales = [&](int p, float &k, float &v) {
+        k = v = 0.f;
+        if (p >= 0) {
+          k = cv.k_scale[static_cast<size_t>(p) * cv.H + sg.h];
+          v = cv.v_scale[static_cast<size_t>(p) * cv.H + sg.h];
         }
-        __syncwarp();
-        ++issued;
+      };
+      fetch_scales(pid, ks, vs);
+      const int gpb = cv.page / 16;                    // groups per page (a page is at most a tile)
+      for (int tb = sg.t0; tb < sg.t1 && ok; tb += 4) {
+        const int npid = fetch_page(8 * (tb + 4) + lane);
+        float nks, nvs;
+        fetch_scales(npid, nks, nvs);
+        for (int t = tb; t < min(tb + 4, sg.t1); ++t, ++it) {
+          const int s = it % NS;
+          const int gl = 8 * (t - tb);                 // lane of the tile's first group
+          ok = mbar_wait_warp(b_empty(s), ((it / NS) & 1) ^ 1, a.wait_ns, abort_flag);
+          if (!ok) break;
+          if (lane >= gl && lane < gl + 8) {
+            float4 f;
+            f.x = ks;
+            f.y = pid >= 0 ? __log2f(vs) : -INFINITY;
+            f.z = pid >= 0 ? 1.f / vs : 0.f;
+            f.w = 0.f;
+            *reinterpret_cast<float4 *>(smem + C::OFF_SC + (s * 8 + lane - gl) * 16) = f;
+          }
+          // the first lane of each page's groups loads it
+          const bool mine = lane >= gl && lane < gl + 8 && (lane - gl) % gpb == 0 && pid >= 0;
+          const unsigned who = __ballot_sync(0xffffffffu, mine);
+          const uint32_t page_bytes = static_cast<uint32_t>(cv.page) * D;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(b_full(s), __popc(who) * 2 * page_bytes);
+          __syncwarp();
+          if (mine) {
+            const uint32_t dst = sbase + C::OFF_KV + s * 2 * C::TILE + (lane - gl) * 16 * D;
+            const int r = static_cast<int>((static_cast<long long>(pid) * cv.H + sg.h) * cv.page);
+            tma_load_2d(dst, &a.tmK, 0, r, b_full(s));
+            tma_load_2d(dst + C::TILE, &a.tmV, 0, r, b_full(s));
+          }
+          __syncwarp();
+        }
+        pid = npid;
+        ks = nks;
+        vs = nvs;
       }
-      pid = npid;
-      ks = nks;
-      vs = nvs;
     }
     if (!ok && lane == 0 && !*abort_flag) {
       *abort_flag = 1;
@@ -243,12 +271,24 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     }
     // never leave the CTA with a copy still landing in its shared memory
     volatile int never = 0;
-    for (int it = (issued > NS ? issued - NS : 0); it < issued; ++it)
-      mbar_wait(b_full(it % NS), (it / NS) & 1, 2000000000ull, &never);
+    for (int i = (it > NS ? it - NS : 0); i < it; ++i)
+      mbar_wait(b_full(i % NS), (i / NS) & 1, 2000000000ull, &never);
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ products and softmax
     const int g = lane >> 2, t = lane & 3;
+    bool ok = true;
+    int it = 0;
+    while (next(sg)) {
+    const int row0 = sg.block * 16 * MT;                 // rows are (token, query head of the group)
+    const int kmax = sg.kmax;
+    // keys that row i of the item sees: [0, limit)
+    auto limit_of = [&](int row) {
+      const int i = row / share;
+      if (row >= sa.n_rows || i >= sg.nq) return 0;
+      return sa.causal ? max(sg.len - sg.nq + i + 1, 0) : sg.len;
+    };
+    const int last_row = min(row0 + 16 * MT, sa.n_rows) - 1;
     uint32_t qa[MT][SEG][4][4];
     float rowf[MT][2];
     int lim[MT][2];
@@ -260,14 +300,15 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
         lim[mt][u] = limit_of(row);
         uint4 w[SEG][2];
 #pragma unroll
-        for (int sg = 0; sg < SEG; ++sg) w[sg][0] = w[sg][1] = make_uint4(0, 0, 0, 0);
-        if (row < n_rows) {
-          const int i = row / a.share, hq = h * a.share + row % a.share;
-          const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + ((static_cast<size_t>(b) * a.Hq + hq) * a.Nq + i) * D);
+        for (int sgm = 0; sgm < SEG; ++sgm) w[sgm][0] = w[sgm][1] = make_uint4(0, 0, 0, 0);
+        if (row < sa.n_rows) {
+          const int i = row / share, hq = sg.h * share + row % share;
+          const uint4 *q = reinterpret_cast<const uint4 *>(
+              a.Q + ((static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i) * D);
 #pragma unroll
-          for (int sg = 0; sg < SEG; ++sg) {
-            w[sg][0] = q[sg * 8 + 2 * t];
-            w[sg][1] = q[sg * 8 + 2 * t + 1];
+          for (int sgm = 0; sgm < SEG; ++sgm) {
+            w[sgm][0] = q[sgm * 8 + 2 * t];
+            w[sgm][1] = q[sgm * 8 + 2 * t + 1];
           }
         }
         // the row's largest magnitude, as bf16 bits
@@ -281,21 +322,20 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         rowf[mt][u] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
-        for (int sg = 0; sg < SEG; ++sg) {
-          const uint32_t *y = reinterpret_cast<const uint32_t *>(w[sg]);
+        for (int sgm = 0; sgm < SEG; ++sgm) {
+          const uint32_t *y = reinterpret_cast<const uint32_t *>(w[sgm]);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const uint32_t z = y[2 * j + p];
-              qa[mt][sg][j][u + 2 * p] =
+              qa[mt][sgm][j][u + 2 * p] =
                   half2_bits(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
             }
         }
       }
-    // keys every row of the CTA sees
-    int all = 0x7FFFFFFF;
-    for (int row = row0; row <= last_row; ++row) all = min(all, limit_of(row));
+    // keys every row of the CTA sees: no row of a block sees fewer than its first (queries behind nq: none)
+    const int all = min(limit_of(row0), limit_of(last_row));
 
     constexpr int NT = D / 8;          // column tiles of O
     float o[MT][NT][4];
@@ -309,11 +349,14 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
       m[mt][0] = m[mt][1] = -INFINITY;
       l[mt][0] = l[mt][1] = 0.f;
     }
-    bool ok = true;
-    for (int tt = t0; tt < t1; ++tt) {
-      const int it = tt - t0, s = it % NS;
+    for (int tt = sg.t0; tt < sg.t1; ++tt, ++it) {
+      const int s = it % NS;
       if (!mbar_wait_warp(b_full(s), (it / NS) & 1, a.wait_ns, abort_flag)) {
         ok = false;
+        if (lane == 0 && !*abort_flag) {     // the others then give up too, before the barriers below
+          *abort_flag = 1;
+          record_status(a.status, kStatusTimeout);
+        }
         break;
       }
       const int key0 = tt * BN + warp * 32;
@@ -333,8 +376,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
             for (int e = 0; e < 4; ++e) sc[mt][i][e] = 0.f;
           const int r = 8 * i + key_of<D>(g);
 #pragma unroll
-          for (int sg = 0; sg < SEG; ++sg) {
-            const int chunk = D == 128 ? ((4 * sg + t) ^ (r & 7)) : (t ^ ((r >> 1) & 3));
+          for (int sgm = 0; sgm < SEG; ++sgm) {
+            const int chunk = D == 128 ? ((4 * sgm + t) ^ (r & 7)) : (t ^ ((r >> 1) & 3));
             const uint4 w = *reinterpret_cast<const uint4 *>(kb + r * D + chunk * 16);
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -342,7 +385,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
               const uint32_t b0 = half2_of_e4m3x2(x[j]), b1 = half2_of_e4m3x2_hi(x[j]);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
-                mma_f16(sc[mt][i], qa[mt][sg][j][0], qa[mt][sg][j][1], qa[mt][sg][j][2], qa[mt][sg][j][3], b0, b1);
+                mma_f16(sc[mt][i], qa[mt][sgm][j][0], qa[mt][sgm][j][1], qa[mt][sgm][j][2], qa[mt][sgm][j][3], b0, b1);
             }
           }
         }
@@ -387,7 +430,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
               o[mt][c][3] *= al[1];
             }
           }
-          const float mu[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0], m[mt][1] == -INFINITY ? 0.f : m[mt][1]};
+          const float mu[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kRowsBias,
+                               m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kRowsBias};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float inv = i < 2 ? sc0.z : sc1.z;
@@ -437,12 +481,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(b_empty(s));
     }
-    if (!ok && lane == 0 && !*abort_flag) {
-      *abort_flag = 1;
-      record_status(a.status, kStatusTimeout);
-    }
-    // all warps of the CTA have read their last tile before the ring is reused
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    // ---- the four warps' parts into the CTA's, 32 numbers of every row at a time:
+    // thread t holds numbers (D / 8)(2t + e) + c of rows g and 8 + g
     float2 *wml = reinterpret_cast<float2 *>(smem + C::OFF_WML);
     float *wo = reinterpret_cast<float *>(smem + C::OFF_WO);
 #pragma unroll
@@ -452,69 +492,123 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
         float s = l[mt][u];
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         s += __shfl_xor_sync(0xffffffffu, s, 2);
-        const int r = warp * 16 * MT + mt * 16 + u * 8 + g;
-        if (t == 0) wml[r] = make_float2(m[mt][u], s);
-        // numbers (D / 8)(2t + e) + c
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int c = 0; c < NT; c += 4)
-            *reinterpret_cast<float4 *>(wo + r * C::OLD + NT * (2 * t + e) + c) =
-                make_float4(o[mt][c][2 * u + e], o[mt][c + 1][2 * u + e], o[mt][c + 2][2 * u + e], o[mt][c + 3][2 * u + e]);
+        if (t == 0)
+          wml[warp * 16 * MT + mt * 16 + u * 8 + g] =
+              make_float2(m[mt][u] == -INFINITY ? -INFINITY : m[mt][u] - kRowsBias, s);
       }
     asm volatile("bar.sync 1, 128;" ::: "memory");
-    // ---- the four warps' parts into the CTA's
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
-    float *oc = reinterpret_cast<float *>(smem + C::OFF_O);
-    for (int idx = tid; idx < 16 * MT * (D / 4); idx += 128) {
-      const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
-      float mm = -INFINITY;
+    // this thread merges 4 numbers of row tid / 8 (and 16 rows on, for the second row tile)
+    float2 ml[MT];
+    float f[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 16 + tid / 8;
+      float mm = -INFINITY, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) mm = fmaxf(mm, wml[w * 16 * MT + r].x);
-      float ll = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 p = wml[w * 16 * MT + r];
-        const float f = p.x == -INFINITY && !(p.y != p.y) ? 0.f : ex2_approx(p.x - mm);
-        const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 16 * MT + r) * C::OLD + c);
-        ll = fmaf(p.y, f, ll);
-        acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+        f[mt][w] = merge_factor(p.x, p.y, mm);
+        ll = fmaf(p.y, f[mt][w], ll);
       }
-      *reinterpret_cast<float4 *>(oc + r * D + c) = acc;
-      if (c == 0) ml[r] = make_float2(mm, ll);
+      ml[mt] = make_float2(mm, ll);
     }
+    const size_t slot = CLUSTER ? 0 : (2 * static_cast<size_t>(rank) + (sg.first ? 1 : 0)) * 16 * MT;
+    if constexpr (!CLUSTER) {
+      if (tid == 0 && sg.first && !sg.whole && ok) {
+        MergeItem mi;
+        mi.b = sg.b;
+        mi.h = sg.h;
+        mi.block = sg.block;
+        mi.go_on = sg.go_on;
+        a.m.items[rank] = mi;
+      }
+    }
+    float2 *cml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    float *oc = reinterpret_cast<float *>(smem + C::OFF_O);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = mt * 16 + tid / 8;
+      if (tid % 8 == 0) {
+        if constexpr (CLUSTER) cml[r] = ml[mt];
+        else if (!sg.whole) a.m.ml[slot + r] = ml[mt];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NT / 4; ++q) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4 *>(wo + (warp * 16 * MT + mt * 16 + u * 8 + g) * C::OLD + 4 * (2 * t + e)) =
+                make_float4(o[mt][4 * q][2 * u + e], o[mt][4 * q + 1][2 * u + e], o[mt][4 * q + 2][2 * u + e],
+                            o[mt][4 * q + 3][2 * u + e]);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = mt * 16 + tid / 8, te = tid % 8, col = NT * te + 4 * q;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 16 * MT + r) * C::OLD + 4 * te);
+          const float y = f[mt][w];
+          acc = make_float4(fmaf(x.x, y, acc.x), fmaf(x.y, y, acc.y), fmaf(x.z, y, acc.z), fmaf(x.w, y, acc.w));
+        }
+        if constexpr (CLUSTER) {
+          *reinterpret_cast<float4 *>(oc + r * D + col) = acc;
+        } else if (!sg.whole) {
+          *reinterpret_cast<float4 *>(a.m.o + (slot + r) * D + col) = acc;
+        } else if (row0 + r < sa.n_rows && ok) {
+          const float inv = ml[mt].y == 0.f ? 0.f : 1.f / ml[mt].y;      // a row that sees nothing is 0
+          const int row = row0 + r, i = row / share, hq = sg.h * share + row % share;
+          const size_t at = (static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i;
+          *reinterpret_cast<uint2 *>(a.O + at * D + col) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          // l is in units of 2^reference: the sum of exp(score) is l 2^reference
+          if (a.lse && te == 0 && q == 0)
+            a.lse[at] = ml[mt].y == 0.f ? -INFINITY : (ml[mt].x + log2f(ml[mt].y)) * 0.6931471805599453f;
+        }
+      }
+      if (q + 1 < NT / 4) asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    if (!group_ok(ok)) break;          // all four warps give up together
+    }   // parts
   }
   // ---------------------------------------------------------------------- merge over the cluster
-  if (ranks > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-  if (!*abort_flag) {
-    const int rows_here = min(16 * MT, n_rows - row0);
-    for (int idx = rank * C::THREADS + tid; idx < rows_here * (D / 4); idx += ranks * C::THREADS) {
-      const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
-      float mm = -INFINITY;
-      for (int k = 0; k < ranks; ++k) mm = fmaxf(mm, ld_dsmem(sbase + C::OFF_ML + r * 8, k));
-      float ll = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < ranks; ++k) {
-        const float pm = ld_dsmem(sbase + C::OFF_ML + r * 8, k), pl = ld_dsmem(sbase + C::OFF_ML + r * 8 + 4, k);
-        const float f = pm == -INFINITY && !(pl != pl) ? 0.f : ex2_approx(pm - mm);
-        const float4 x = ld_dsmem4(sbase + C::OFF_O + (r * D + c) * 4, k);
-        ll = fmaf(pl, f, ll);
-        acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+  if constexpr (CLUSTER) {
+    if (ranks > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    if (!*abort_flag) {
+      const int row0 = run.block * 16 * MT;
+      const int rows_here = min(16 * MT, sa.n_rows - row0);
+      for (int idx = rank * C::THREADS + tid; idx < rows_here * (D / 4); idx += ranks * C::THREADS) {
+        const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
+        float mm = -INFINITY;
+        for (int k = 0; k < ranks; ++k) mm = fmaxf(mm, ld_dsmem(sbase + C::OFF_ML + r * 8, k));
+        float ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < ranks; ++k) {
+          const float pm = ld_dsmem(sbase + C::OFF_ML + r * 8, k), pl = ld_dsmem(sbase + C::OFF_ML + r * 8 + 4, k);
+          const float f = merge_factor(pm, pl, mm);
+          const float4 x = ld_dsmem4(sbase + C::OFF_O + (r * D + c) * 4, k);
+          ll = fmaf(pl, f, ll);
+          acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+        }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;      // a row that sees nothing is 0
+        const int row = row0 + r, i = row / share, hq = run.h * share + row % share;
+        const size_t at = (static_cast<size_t>(run.b) * sa.H * share + hq) * sa.Nq + i;
+        *reinterpret_cast<uint2 *>(a.O + at * D + c) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (c == 0 && a.lse) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
       }
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;      // a row that sees nothing is 0
-      const int row = row0 + r, i = row / a.share, hq = h * a.share + row % a.share;
-      const size_t at = (static_cast<size_t>(b) * a.Hq + hq) * a.Nq + i;
-      *reinterpret_cast<uint2 *>(a.O + at * D + c) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      // l is in units of 2^m: the sum of exp(score) is l 2^m
-      if (c == 0 && a.lse) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
     }
+    if (ranks > 1) cluster_sync();   // no CTA leaves while another reads it
   }
-  if (ranks > 1) cluster_sync();   // no CTA leaves while another reads it
 }
 
 }  // namespace mcs

@@ -61,7 +61,8 @@ def test_a_cache_that_is_none(L, bad, code):
     s = I64x3(0, 0, 64)
     assert L.mcs_cache_append(c, FAKE, FAKE, s, s, 1, FAKE, None, None, 0, 0, None, None) == code
     assert L.mcs_cache_read(c, FAKE, None, 1, FAKE, FAKE, None) == code
-    assert L.mcs_cache_attention(c, FAKE, 2, 1, FAKE, None, 0, 0.125, FAKE, None, None) == code
+    assert L.mcs_cache_attention(c, FAKE, 2, 1, FAKE, None, 0, 0.125, FAKE, None, FAKE, 2 ** 30, None) == code
+    assert L.mcs_cache_attention_workspace_size(c, 2, 1) == 0
 
 
 def test_append_read_attention(L):
@@ -84,12 +85,12 @@ def test_append_read_attention(L):
                 (FAKE, None, 1, FAKE + 2, FAKE), (FAKE, None, 1, FAKE, None)):
         assert L.mcs_cache_read(c, *bad, None) == INVALID
 
-    def attend(Q=FAKE, Hq=4, Nq=1, lengths=FAKE, counts=None, scale=0.125, O=FAKE, lse=None):
-        return L.mcs_cache_attention(c, Q, Hq, Nq, lengths, counts, 0, scale, O, lse, None)
+    def attend(Q=FAKE, Hq=4, Nq=1, lengths=FAKE, counts=None, scale=0.125, O=FAKE, lse=None, ws=FAKE):
+        return L.mcs_cache_attention(c, Q, Hq, Nq, lengths, counts, 0, scale, O, lse, ws, 2 ** 30, None)
     assert attend(Nq=0) == OK
     for bad in (dict(Q=None), dict(O=None), dict(lengths=None), dict(Hq=3), dict(Hq=0), dict(Nq=-1), dict(scale=0.0),
                 dict(scale=float("nan")), dict(Q=FAKE + 8), dict(counts=FAKE + 2), dict(lse=FAKE + 1),
-                dict(Nq=2 ** 20, Hq=4)):
+                dict(ws=FAKE + 8), dict(Nq=2 ** 20, Hq=4)):
         assert attend(**bad) == INVALID
 
 

@@ -177,6 +177,14 @@ CASES = [
     (2, 2, 1, 512, 128, 128, [129, 1537], True, [512, 400]),
     (1, 5, 5, 256, 64, 64, [128], False, None),
     (1, 4, 1, 700, 128, 32, [11], True, None),
+    # enough places for the work to be dealt over all SMs: lengths far apart, parts that end anywhere
+    (5, 4, 2, 1, 64, 16, [8300, 1, 0, 700, 4097], True, None),
+    (1, 3, 1, 1, 128, 128, [20001], False, None),
+    (2, 4, 2, 10, 128, 32, [8193, 8200], True, [10, 3]),
+    (9, 2, 2, 1, 64, 64, [9000, 0, 0, 130, 129, 128, 127, 1, 8000], False, None),
+    (40, 8, 8, 1, 64, 16, [(37 * i * i) % 700 for i in range(40)], True, None),
+    (2, 2, 1, 300, 64, 16, [8400, 299], True, [300, 299]),
+    (1, 3, 3, 400, 128, 64, [400], True, None),
 ]
 
 
