@@ -14,7 +14,8 @@ SOURCES = ["mcs_api.cu", "cache_api.cu"]
 MICRO_SOURCES = ["micro_gather.cu", "micro_pipes.cu"]
 HEADERS = ["mcs_common.cuh", "ablation_kernels.cuh", "attn_kernel.cuh", "attn_dual_kernel.cuh", "pair_kernel.cuh", "colsum_kernel.cuh", "topk_kernel.cuh",
            "group_kernels.cuh", "validate_kernels.cuh", "residual_compact.cuh", "rotary.cuh", "kvcache_kernels.cuh",
-           "cache_sched.cuh", "cache_rows_kernel.cuh", "host_shared.h"]
+           "cache_sched.cuh", "cache_rows_kernel.cuh", "cache_tile_kernel.cuh",
+           "host_shared.h"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

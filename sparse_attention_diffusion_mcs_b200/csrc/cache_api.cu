@@ -5,9 +5,11 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/mcs.h"
 #include "cache_rows_kernel.cuh"
+#include "cache_tile_kernel.cuh"
 #include "host_shared.h"
 #include "kvcache_kernels.cuh"
 #include "rotary.cuh"
@@ -117,15 +119,15 @@ constexpr int kMaxCtas = 2 * 148;
 
 // sizes of one call: blocks of rows, and how they are computed
 struct AttnPlan {
-  int mt;                        // row tiles of 16 of a block (cache_rows_kernel)
+  int mt;                        // row tiles of 16 of a block (cache_rows_kernel); 0: cache_tile_kernel
   int rows;                      // rows of a block
   int ctas;                      // CTAs that share the work; 0: clusters, no workspace
   int split;                     // CTAs of a cluster
 };
 AttnPlan plan_attention(const CacheView &c, int B, long long n_rows, int sms) {
   AttnPlan p;
-  p.mt = n_rows <= 16 ? 1 : 2;
-  p.rows = 16 * p.mt;
+  p.mt = n_rows <= 16 ? 1 : n_rows <= 32 ? 2 : 0;
+  p.rows = p.mt ? 16 * p.mt : 256;
   const long long blocks = (n_rows + p.rows - 1) / p.rows;
   const long long items = static_cast<long long>(B) * c.H * blocks;
   const long long tiles = (static_cast<long long>(c.max_pages) * c.page + kKeyTile - 1) / kKeyTile;
@@ -135,7 +137,7 @@ AttnPlan plan_attention(const CacheView &c, int B, long long n_rows, int sms) {
   // Little work (by the table's places; lengths are not known here): clusters
   // of 8 CTAs (the portable size) at most, as many as fill the SMs once and as
   // there can be tiles.
-  if (blocks <= 65535 && tiles <= 64 && items * tiles <= 16ll * sms) {
+  if (p.mt && tiles <= 64 && items * tiles <= 16ll * sms) {
     long long split = resident / items;
     split = split > 8 ? 8 : split;
     split = split > tiles ? tiles : split;
@@ -171,6 +173,20 @@ cudaError_t launch_rows(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, 
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cache_rows_kernel<D, MT, true>, a);
+}
+
+template <int D>
+cudaError_t launch_tile(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, cudaStream_t s) {
+  using C = TileCfg<D>;
+  const cudaError_t e = allow_smem<cache_tile_kernel<D>>(dev, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cache_tile_kernel<D><<<p.ctas, C::THREADS, C::SMEM, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_attention(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, cudaStream_t s) {
+  return p.mt == 1 ? launch_rows<D, 1>(a, p, dev, s) : p.mt == 2 ? launch_rows<D, 2>(a, p, dev, s) : launch_tile<D>(a, p, dev, s);
 }
 
 template <int D>
@@ -356,11 +372,7 @@ mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, in
   const size_t rows = static_cast<size_t>(a.c.n_pages) * a.c.H * a.c.page;
   if (!map_byte_rows(&a.tmK, a.c.k, a.c.d, rows, a.c.page) || !map_byte_rows(&a.tmV, a.c.v, a.c.d, rows, a.c.page))
     return MCS_ERR_CUDA;
-  cudaError_t e;
-  if (a.c.d == 64)
-    e = p.mt == 1 ? launch_rows<64, 1>(a, p, dev, cu(stream)) : launch_rows<64, 2>(a, p, dev, cu(stream));
-  else
-    e = p.mt == 1 ? launch_rows<128, 1>(a, p, dev, cu(stream)) : launch_rows<128, 2>(a, p, dev, cu(stream));
+  cudaError_t e = a.c.d == 64 ? launch_attention<64>(a, p, dev, cu(stream)) : launch_attention<128>(a, p, dev, cu(stream));
   if (e == cudaSuccess && p.ctas) e = a.c.d == 64 ? launch_merge<64>(a, p, cu(stream)) : launch_merge<128>(a, p, cu(stream));
   return cuda_status(e);
 }

@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
         const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         rowf[mt][u] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (am >> 8 == 255) rowf[mt][u] = __uint_as_float(0x7FC00000u);   // a query that is not finite: NaN
 #pragma unroll
         for (int sgm = 0; sgm < SEG; ++sgm) {
           const uint32_t *y = reinterpret_cast<const uint32_t *>(w[sgm]);
