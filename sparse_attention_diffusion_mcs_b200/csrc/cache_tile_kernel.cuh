@@ -12,7 +12,7 @@
 // Two 8-bit products (hi, then lo) cost what one 16-bit product costs, and no
 // key is converted.
 // P.V runs in fp16: the weights need more than e4m3's 4 bits, and a weight
-// whose 8-bit parts underflow would lose the tail of a long row.  Two warps
+// whose 8-bit parts underflow would lose the tail of a long row.  Four warps
 // turn each 128-key tile of V into fp16 once (exact) for all 256 query rows.
 // Weights are 2^(y - m + 6) with m at most 2^8 behind the row's maximum: at
 // most 2^14, rounded to fp16 by 2^-11 relative, normal down to 2^-20 of the
@@ -20,28 +20,62 @@
 //
 // A CTA takes 256 query rows (two halves of 128, one TMEM lane a row) and runs
 // of 128-key tiles, dealt as cache_sched.cuh describes:
-//   warps 0-3, 4-7  softmax and epilogue of half 0, half 1
-//   warp  8         TMEM allocation, the single MMA-issuing thread
-//   warp  9         loads: one TMA box per page, keys and values; the scales
-//   warps 10, 11    V from e4m3 to fp16
+//   warp  0         TMEM allocation, MMA issue
+//   warp  1         loads: one TMA box per page, keys and values; the scales
+//   warps 4-7       V from e4m3 to fp16
+//   warps 8-11, 12-15  softmax and epilogue of half 0, half 1
 // The tensor pipe runs per tile j: PV0(j) QK0(j+1) PV1(j) QK1(j+1), so each
-// half's softmax has the other half's two products to work in.  P (fp16 pairs)
-// lies over the upper half of its own S.  TMEM: S0, S1 (128 columns each),
-// O0, O1 (D columns each).  Every wait is bounded.
+// half's softmax has the other half's two products to work in.  A block of at
+// most 128 rows has no second half: the two then take alternate tiles of the
+// same rows, and half 0 adds half 1's O to its own at the end (PV0(j) QK0(j+2)
+// PV1(j+1) QK1(j+3)).  P (fp16 pairs) lies over the lower half of its own S.
+// TMEM: S0, S1 (128 columns each), O0, O1 (D columns each).  Every wait is
+// bounded.
+//
+// Measured (4680 causal rows against 32760 tokens, 24 heads of 128): 1.72 ms,
+// 1.02 PFLOP/s; the same without the conversion of V 1.63, without
+// exponentials 1.47 ms.  Per tile a half's softmax takes 2600 cycles beside the
+// other half's (1024 of them exponentials), and the products 2340 instead of
+// 2048: they, the conversion and the loads ask for 2330 cycles of the shared
+// memory's 128 bytes a cycle.  Tried and slower: one thread per half row (1.83),
+// S read twice (1.86), tiles of 64 keys with S double-buffered (1.87: twice
+// the MMA instructions, 75 cycles each to issue), an MMA warp per half (2.13:
+// both halves' products then end late, together), exponentials on the FMA
+// pipe (one in eight 1.81, one in four 1.98).
 #pragma once
 
 #include "cache_rows_kernel.cuh"
 
 namespace mcs {
 
-// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulate.
-__device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The MMA warp's lanes run its loop together, so that operands stay in uniform
+// registers; each instruction is issued by one elected lane.
+
+// the same word of every lane as a warp-uniform one
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulate; descriptors by their halves.
+__device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Instruction descriptors: e4m3 (kind::f8f6f4) and fp16 (kind::f16), fp32 D.
@@ -70,16 +104,11 @@ __device__ __forceinline__ int swizzled(int row, int chunk) {
   return row * ROW + ((ROW == 128 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-// maxima that keep NaN
-__device__ __forceinline__ float fmax_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
+// the largest of 16 numbers
+__device__ __forceinline__ float max16(const float *x) {
+  const float a = fmax3(x[0], x[1], x[2]), b = fmax3(x[3], x[4], x[5]), c = fmax3(x[6], x[7], x[8]);
+  const float d = fmax3(x[9], x[10], x[11]), e = fmax3(x[12], x[13], x[14]);
+  return fmaxf(fmax3(a, b, c), fmax3(d, e, x[15]));
 }
 
 template <int D>
@@ -97,13 +126,13 @@ struct TileCfg {
   static constexpr int OFF_H = OFF_V + NV * T8;
   static constexpr int OFF_SC = OFF_H + NH * T16;             // per tile: 8 x float4 (ks, log2 vs, 1 / vs, whole tile)
   static constexpr int OFF_BAR = OFF_SC + NSC * 8 * 16;
-  static constexpr int N_BAR = 2 * NK + 2 * NV + 2 * NH + NSC + 8 + 1;
-  static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
+  static constexpr int N_BAR = 2 * NK + 2 * NV + 2 * NH + NSC + 10 + 1;
+  static constexpr int OFF_XCH = OFF_BAR + 8 * N_BAR;         // 128 x float2: half 1's reference and sum for half 0
+  static constexpr int OFF_MISC = OFF_XCH + BM * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CVT_WARP = 10, CVT_THREADS = 64;
-  static constexpr int THREADS = 12 * 32;
+  static constexpr int MMA_WARP = 0, LOAD_WARP = 1, CVT_WARP = 4, CVT_THREADS = 128, SOFTMAX_WARP = 8;
+  static constexpr int THREADS = 16 * 32;
   static constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_O = 256;   // half h: S at 128 h, O at 256 + D h
-  static constexpr uint32_t COL_P = 64;           // of S
   static constexpr float kBias = 6.f, kRaise = 8.f;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -132,7 +161,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
   auto b_s = [&](int h) { return by + 16 + 8 * h; };
   auto b_p = [&](int h) { return by + 32 + 8 * h; };
   auto b_o = [&](int h) { return by + 48 + 8 * h; };
-  const uint32_t b_drain = by + 64;
+  auto b_j = [&](int h) { return by + 64 + 8 * h; };
+  const uint32_t b_drain = by + 80;
+  float2 *xch = reinterpret_cast<float2 *>(smem + C::OFF_XCH);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
 
@@ -147,24 +178,25 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
     }
     for (int i = 0; i < NV; ++i) {
       mbar_init(b_vfull(i), 1);
-      mbar_init(b_vempty(i), C::CVT_THREADS);
+      mbar_init(b_vempty(i), C::CVT_THREADS / 32);
     }
     for (int i = 0; i < NH; ++i) {
-      mbar_init(b_hfull(i), C::CVT_THREADS);
+      mbar_init(b_hfull(i), C::CVT_THREADS / 32);
       mbar_init(b_hempty(i), 1);
     }
     for (int i = 0; i < NSC; ++i) mbar_init(b_sc(i), 1);
     for (int h = 0; h < 2; ++h) {
-      mbar_init(b_q(h), 128);
+      mbar_init(b_q(h), 4);
       mbar_init(b_s(h), 1);
-      mbar_init(b_p(h), 128);
+      mbar_init(b_p(h), 4);                        // (one lane a warp)
       mbar_init(b_o(h), 1);
+      mbar_init(b_j(h), 4);
     }
     mbar_init(b_drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
-    a.m.items[cta].go_on = 0;
   }
+  if (tid == C::SOFTMAX_WARP * 32) a.m.items[cta].go_on = 0;   // (the thread that may set it)
   if (warp == C::MMA_WARP) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
@@ -175,7 +207,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-
   Segment sg = {};
   // the part's key tiles to read: [t0, end)
   auto end_of = [&]() { return min(sg.t1, (sg.kmax + BN - 1) / BN); };
@@ -186,6 +217,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
     }
   };
 
+  auto warp_arrive = [&](uint32_t bar) {           // once for the warp, when all its lanes are there
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    __syncwarp();
+  };
+  // registers go from the helpers to the softmax, whose threads hold a whole row
+  // of S: 256 x 200 + 256 x 56 = the 512 x 128 of the launch
+  if (warp < C::SOFTMAX_WARP) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------------ loads
     // lane l holds page and scales of the 16-key group 32 bt + l of batch bt
@@ -275,11 +315,19 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
     __syncwarp();
   } else if (warp >= C::CVT_WARP) {
     // ------------------------------------------------------------------ V to fp16
-    // A thread takes 16 numbers of a key at a time: one 16-byte read, two 16-byte
-    // writes.  Eight neighbouring threads take four chunks of keys r and r ^ 5,
-    // which the swizzles of both layouts send to different banks.
-    constexpr int CH = D / 16, PER = BN * CH / C::CVT_THREADS;
-    const int ct = tid - C::CVT_WARP * 32;
+    // A thread takes one 16-byte chunk of every RSTEP-th key: a 16-byte read, two
+    // 16-byte writes at fixed distances.  Eight neighbouring threads take four
+    // chunks of keys r and r ^ 5, which the swizzles of both layouts send to
+    // different banks.
+    constexpr int CH = D / 16, PER = BN * CH / C::CVT_THREADS, RSTEP = BN / PER;
+    static_assert(RSTEP % 8 == 0 && PER % 4 == 0, "a thread's keys share their swizzle");
+    const int ct = tid - C::CVT_WARP * 32;                   // (pair of keys, 4 chunks, key of the pair, chunk)
+    const int rest = ct >> 3, chunk = rest % (CH / 4) * 4 + (ct & 3), pair = rest / (CH / 4);
+    const int key = ((pair >> 2) * 8 + (pair & 3)) ^ (ct & 4 ? 5 : 0);   // pairs (r, r ^ 5), r = 0, 1, 2, 3 of each 8 keys
+    const int from = swizzled<D>(key, chunk);
+    // 64-number blocks of 128-byte rows
+    const int to0 = (chunk >> 2) * (BN * 128) + swizzled<128>(key, 2 * (chunk & 3));
+    const int to1 = (chunk >> 2) * (BN * 128) + swizzled<128>(key, 2 * (chunk & 3) + 1);
     bool ok = true;
     int it = 0;
     while (ok && run.next(sa, sg)) {
@@ -292,115 +340,143 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
         uint8_t *dst = smem + C::OFF_H + (it % NH) * C::T16;
         const float4 *sc = reinterpret_cast<const float4 *>(smem + C::OFF_SC) + (it % NSC) * 8;
         const bool whole = sc[0].w != 0.f && (t + 1) * BN <= sg.kmax;
-#pragma unroll 4
-        for (int i = 0; i < PER; ++i) {
-          const int id = ct + i * C::CVT_THREADS;            // (pair of keys, 4 chunks, key of the pair, chunk)
-          const int c4 = id & 3, second = (id >> 2) & 1, rest = id >> 3;
-          const int q4 = rest % (CH / 4), pair = rest / (CH / 4);
-          // pairs (r, r ^ 5) of 8 keys: r = 0, 1, 2, 3 (bit 2 clear)
-          const int r0 = (pair >> 2) * 8 + (pair & 3), r = second ? r0 ^ 5 : r0, c = q4 * 4 + c4;
-          uint4 w = *reinterpret_cast<const uint4 *>(src + swizzled<D>(r, c));
+        // four reads on the way at once: the compiler cannot move one over the writes of another
+#pragma unroll
+        for (int i0 = 0; i0 < PER; i0 += 4) {
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + from + (i0 + i) * RSTEP * D);
           // what lies behind the last key that is seen, or was never loaded, may be any bits
-          if (!whole && !(t * BN + r < sg.kmax && sc[r >> 4].y > -INFINITY)) w = make_uint4(0, 0, 0, 0);
-          // 64-number blocks of 128-byte rows
-          uint8_t *o = dst + (c >> 2) * (BN * 128);
-          *reinterpret_cast<uint4 *>(o + swizzled<128>(r, 2 * (c & 3))) =
-              make_uint4(half2_of_e4m3x2(w.x), half2_of_e4m3x2_hi(w.x), half2_of_e4m3x2(w.y), half2_of_e4m3x2_hi(w.y));
-          *reinterpret_cast<uint4 *>(o + swizzled<128>(r, 2 * (c & 3) + 1)) =
-              make_uint4(half2_of_e4m3x2(w.z), half2_of_e4m3x2_hi(w.z), half2_of_e4m3x2(w.w), half2_of_e4m3x2_hi(w.w));
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = key + (i0 + i) * RSTEP;
+              if (!(t * BN + r < sg.kmax && sc[r >> 4].y > -INFINITY)) w[i] = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 x = w[i];
+            *reinterpret_cast<uint4 *>(dst + to0 + (i0 + i) * RSTEP * 128) =
+                make_uint4(half2_of_e4m3x2(x.x), half2_of_e4m3x2_hi(x.x), half2_of_e4m3x2(x.y), half2_of_e4m3x2_hi(x.y));
+            *reinterpret_cast<uint4 *>(dst + to1 + (i0 + i) * RSTEP * 128) =
+                make_uint4(half2_of_e4m3x2(x.z), half2_of_e4m3x2_hi(x.z), half2_of_e4m3x2(x.w), half2_of_e4m3x2_hi(x.w));
+          }
         }
         fence_proxy_async_smem();
-        mbar_arrive(b_hfull(it));
-        mbar_arrive(b_vempty(it));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(b_hfull(it));
+          mbar_arrive(b_vempty(it));
+        }
+        __syncwarp();
       }
     }
     if (!ok && lane == 0) give_up();
   } else if (warp == C::MMA_WARP) {
     // ------------------------------------------------------------------ MMA issue
-    if (lane == 0) {
+    {
       constexpr uint32_t idesc_qk = idesc_e4m3_f32(C::BM, BN);
       constexpr uint32_t idesc_pv = idesc_f16_f32(C::BM, D, 1);
+      // descriptors: the upper words are the layouts', the lower ones move with the address
+      const uint64_t dq = sdesc_rows<D>(sbase + C::OFF_Q), dk = sdesc_rows<D>(sbase + C::OFF_K);
+      const uint64_t dv = sdesc_sw128(sbase + C::OFF_H, BN * 128, 1024);
+      const uint32_t q_lo = uniform(static_cast<uint32_t>(dq)), k_lo = uniform(static_cast<uint32_t>(dk));
+      const uint32_t v_lo = uniform(static_cast<uint32_t>(dv));
+      const uint32_t qk_hi = uniform(static_cast<uint32_t>(dq >> 32)), v_hi = uniform(static_cast<uint32_t>(dv >> 32));
+      const uint32_t tb = uniform(tbase);
       bool ok = true;
       int it = 0;                                    // tiles so far, over all parts
       int n_s[2] = {0, 0}, n_part[2] = {0, 0};       // a half's tiles and parts so far
       auto wait = [&](uint32_t bar, int phase) {
-        if (ok) ok = mbar_wait(bar, phase & 1, a.wait_ns, abort_flag);
+        if (ok) ok = mbar_wait_warp(bar, phase & 1, a.wait_ns, abort_flag);
         return ok;
       };
       auto qk = [&](int h, int i) {
-        const uint32_t q = sbase + C::OFF_Q + h * 2 * C::Q_BYTES, k = sbase + C::OFF_K + (i % NK) * C::T8;
-        const uint32_t s = tbase + C::COL_S + 128 * h;
+        const uint32_t q = q_lo + uniform(h * (2 * C::Q_BYTES >> 4)), k = k_lo + uniform(i % NK * (C::T8 >> 4));
+        const uint32_t s = tb + uniform(C::COL_S + 128 * h);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            umma_e4m3_ss(s, sdesc_rows<D>(q + part * C::Q_BYTES + kk * 32), sdesc_rows<D>(k + kk * 32), idesc_qk,
+            umma_e4m3_ss(s, q + ((part * C::Q_BYTES + kk * 32) >> 4), k + (kk * 32 >> 4), qk_hi, idesc_qk,
                          part + kk > 0 ? 1u : 0u);
-        umma_commit(b_s(h));
+        umma_commit_elect(b_s(h));
       };
       auto pv = [&](int h, int i, bool add) {
-        const uint32_t v = sbase + C::OFF_H + (i % NH) * C::T16;
-        const uint32_t p = tbase + C::COL_S + 128 * h + C::COL_P, o = tbase + C::COL_O + D * h;
+        const uint32_t v = v_lo + uniform(i % NH * (C::T16 >> 4));
+        const uint32_t p = tb + uniform(C::COL_S + 128 * h), o = tb + uniform(C::COL_O + D * h);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          umma_bf16_ts(o, p + kk * 8, sdesc_sw128(v + kk * 16 * 128, BN * 128, 1024), idesc_pv, add || kk > 0 ? 1u : 0u);
+          umma_f16_ts(o, p + kk * 8, v + (kk * 16 * 128 >> 4), v_hi, idesc_pv, add || kk > 0 ? 1u : 0u);
       };
       while (ok && run.next(sa, sg)) {
         const int n = end_of() - sg.t0;
         if (n <= 0) continue;
-        wait(b_kfull(it), it / NK);
-        for (int h = 0; h < sg.halves && ok; ++h) {
-          if (!wait(b_q(h), n_part[h])) break;
+        const bool two = sg.halves == 2;
+        // scores of the part's tile j for half h
+        auto scores = [&](int h, int j) {
+          if (!wait(b_kfull(it + j), (it + j) / NK)) return;
+          if (j < (two ? 1 : 2) && !wait(b_q(h), n_part[h])) return;
           tc_fence_after();
-          qk(h, it);
-        }
-        if (!ok) break;
-        umma_commit(b_kempty(it));
-        for (int j = 0; j < n && ok; ++j, ++it) {
-          const bool more = j + 1 < n;
-          if (!wait(b_hfull(it), it / NH)) break;
-          if (more && !wait(b_kfull(it + 1), (it + 1) / NK)) break;
-          for (int h = 0; h < sg.halves && ok; ++h) {
+          qk(h, it + j);
+          if (!two || h == 1) umma_commit_elect(b_kempty(it + j));
+        };
+        scores(0, 0);
+        if (two) scores(1, 0);
+        else if (n > 1) scores(1, 1);
+        for (int j = 0; j < n && ok; ++j) {
+          if (!wait(b_hfull(it + j), (it + j) / NH)) break;
+          const int ahead = two ? 1 : 2;
+          for (int h = two ? 0 : j & 1; h < (two ? 2 : (j & 1) + 1) && ok; ++h) {
             if (!wait(b_p(h), n_s[h])) break;
             ++n_s[h];
             tc_fence_after();
-            pv(h, it, j > 0);
-            if (!more) umma_commit(b_o(h));
-            if (h + 1 == sg.halves) umma_commit(b_hempty(it));
-            if (more) qk(h, it + 1);                 // over S and P of the tile whose P.V is ahead in the pipe
+            pv(h, it + j, j >= ahead);
+            if (j + ahead >= n) umma_commit_elect(b_o(h));
+            if (!two || h == 1) umma_commit_elect(b_hempty(it + j));
+            if (j + ahead < n) scores(h, j + ahead);   // over S and P of the tile whose P.V is ahead in the pipe
           }
-          if (more && ok) umma_commit(b_kempty(it + 1));
         }
-        for (int h = 0; h < sg.halves; ++h) ++n_part[h];
+        it += n;
+        ++n_part[0];
+        if (two || n > 1) ++n_part[1];
       }
-      if (!ok) give_up();
+      if (!ok && lane == 0) give_up();
       // make sure nothing issued is still running before TMEM is released
-      umma_commit(b_drain);
+      umma_commit_elect(b_drain);
       volatile int never = 0;
       mbar_wait(b_drain, 0, 2000000000ull, &never);
     }
     __syncwarp();
+  }
   } else {
     // ------------------------------------------------------------------ softmax
-    const int half = warp >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int half = (warp - C::SOFTMAX_WARP) >> 2;
     const int r = (warp & 3) * 32 + lane;              // row of the half == TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + lane_addr + C::COL_S + 128 * half, tP = tS + C::COL_P;
+    const uint32_t tS = tbase + lane_addr + C::COL_S + 128 * half;
     const uint32_t tO = tbase + lane_addr + C::COL_O + D * half;
     const int share = sa.share;
     bool ok = true;
-    int it = 0, n_s = 0, n_part = 0;                   // all tiles so far; this half's tiles and parts
+    int it = 0, n_s = 0, n_part = 0, n_join = 0;       // all tiles so far; this half's tiles and parts; joint parts
     while (ok && run.next(sa, sg)) {
-      const int end = end_of(), n = max(end - sg.t0, 0);
-      const int row0 = sg.block * C::ROWS + half * C::BM, row = row0 + r;
+      const int end = end_of(), n = max(end - sg.t0, 0), it0 = it;
+      const bool two = sg.halves == 2;
+      const int row0 = sg.block * C::ROWS + (two ? half * C::BM : 0), row = row0 + r;   // whose scores
+      const int orow = sg.block * C::ROWS + half * C::BM + r;                             // whose output
       auto limit_of = [&](int x) {                     // keys that row x sees: [0, limit)
         const int i = x / share;
         if (x >= sa.n_rows || i >= sg.nq) return 0;
         return sa.causal ? max(sg.len - sg.nq + i + 1, 0) : sg.len;
       };
-      const bool active = half < sg.halves && n > 0;
-      const int qi = row / share, hq = sg.h * share + row % share;
-      const size_t at = (static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + qi;   // row of Q and O
+      const int step = two ? 1 : 2, skip = two ? 0 : half;   // this half's tiles: t0 + skip, + step, ...
+      const bool active = n > skip;
+      auto address = [&](int x) {                      // row x of the item in Q and O
+        const int i = x / share, hq = sg.h * share + x % share;
+        return (static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i;
+      };
       float m_run = -INFINITY, l_run = 0.f;
       if (active) {
         // ---- the row's query in two e4m3 parts
@@ -410,7 +486,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
           if (row < sa.n_rows) {
-            const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + at * D);
+            const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + address(row) * D);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
           }
@@ -449,11 +525,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
             *reinterpret_cast<uint4 *>(qs + C::Q_BYTES + swizzled<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
           fence_proxy_async_smem();
-          mbar_arrive(b_q(half));
+          warp_arrive(b_q(half));
         }
         const int lim = limit_of(row);
         const int all = min(limit_of(row0), limit_of(min(row0 + C::BM, sa.n_rows) - 1));   // keys every row sees
-        for (int t = sg.t0; t < end; ++t, ++it, ++n_s) {
+        it += skip;
+        for (int t = sg.t0 + skip; t < end; t += step, it += step, ++n_s) {
           if (!mbar_wait_warp(b_s(half), n_s & 1, a.wait_ns, abort_flag) ||
               !mbar_wait_warp(b_sc(it), (it / NSC) & 1, a.wait_ns, abort_flag)) {
             ok = false;
@@ -464,40 +541,28 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           const int left = lim - t * BN;               // columns that this row sees
           auto tile = [&](auto clean_tag) {
             constexpr bool CLEAN = decltype(clean_tag)::value;
-            float v[64];
-            // ---- the row's largest y; columns 64.. stay in registers
+            // the whole row in registers: a read of S takes hundreds of cycles beside the products
+            float v[128];
+            tmem_ld64(tS, *reinterpret_cast<float(*)[64]>(v));
+            tmem_ld64(tS + 64, *reinterpret_cast<float(*)[64]>(v + 64));
+            tmem_wait_ld();
+            // ---- the row's largest y
             float mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tmem_ld64(tS + 64 * c, v);
-              tmem_wait_ld();
+            for (int g = 0; g < 8; ++g) {
+              const float4 f = sc[g];
+              if (!CLEAN) {
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float4 f = sc[4 * c + g];
-                if (!CLEAN) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    v[16 * g + i] = 64 * c + 16 * g + i < left && f.y > -INFINITY ? v[16 * g + i] : -INFINITY;
-                }
-                float m0 = v[16 * g], m1 = v[16 * g + 1];
-#pragma unroll
-                for (int i = 2; i < 14; i += 4) {
-                  m0 = fmax3_nan(m0, v[16 * g + i], v[16 * g + i + 1]);
-                  m1 = fmax3_nan(m1, v[16 * g + i + 2], v[16 * g + i + 3]);
-                }
-                m0 = fmax3_nan(m0, v[16 * g + 14], v[16 * g + 15]);
-                m0 = fmax_nan(m0, m1);
-                float y = fmaf(m0, rowf * f.x, f.y);
-                if (!CLEAN) y = m0 == -INFINITY ? -INFINITY : y;
-                mx = fmax_nan(mx, y);
+                for (int i = 16 * g; i < 16 * g + 16; ++i) v[i] = i < left && f.y > -INFINITY ? v[i] : -INFINITY;
               }
+              const float top = max16(v + 16 * g), y = fmaf(top, rowf * f.x, f.y);
+              mx = fmaxf(mx, CLEAN || top > -INFINITY ? y : -INFINITY);
             }
-            if (mx != mx) rowf = mx;                   // NaN from here on
             const bool up = mx > m_run + C::kRaise;    // first keys of the row: always (m_run = -inf)
             if (__any_sync(0xffffffffu, up)) {
               const float alpha = up ? ex2_approx(m_run - mx) : 1.f;
               l_run *= alpha;
-              if (t > sg.t0) {   // O holds the tiles before this one: their products are behind this S in the pipe
+              if (t >= sg.t0 + step) {   // O holds the tiles before this one: their products are behind this S in the pipe
 #pragma unroll 1
                 for (int cc = 0; cc < D / 16; ++cc) {
                   float o[16];
@@ -511,69 +576,103 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
               }
               if (up) m_run = mx;
             }
-            // ---- weights, their sum (in units of 1 / vs) and P, columns 64.. first
+            // ---- weights, their sum (in units of 1 / vs) and P, 32 keys at a time, in
+            // stages, so that the exponentials follow one another without a pause (348
+            // cycles for the 32 columns of a warp alone, 628 pair by pair)
             const float ref = m_run == -INFINITY ? 0.f : m_run - C::kBias;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int c = 1 - k;
-              if (c == 0) {
-                tmem_ld64(tS, v);
-                tmem_wait_ld();
-              }
-              uint32_t pk[32];
+            for (int c = 0; c < 4; ++c) {
+              const float4 fs[2] = {sc[2 * c], sc[2 * c + 1]};
+              float2 y[16];
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float4 f = sc[4 * c + g];
-                const float rk = rowf * f.x, off = f.y - ref;
-                const float2 rk2 = make_float2(rk, rk), off2 = make_float2(off, off);
-                float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int e = 16 * g + 2 * i;
-                  float2 x = __ffma2_rn(make_float2(v[e], v[e + 1]), rk2, off2);
-                  if (!CLEAN) {
-                    const int col = 64 * c + e;
-                    x.x = col < left && f.y > -INFINITY ? x.x : -INFINITY;
-                    x.y = col + 1 < left && f.y > -INFINITY ? x.y : -INFINITY;
-                  }
-                  x.x = ex2_approx(x.x);
-                  x.y = ex2_approx(x.y);
-                  sum = __fadd2_rn(sum, x);
-                  pk[8 * g + i] = half2_bits(x.x, x.y);
+              for (int i = 0; i < 16; ++i) {
+                const float rk = rowf * fs[i >> 3].x, off = fs[i >> 3].y - ref;
+                const float2 x = make_float2(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]);
+                y[i] = __ffma2_rn(x, make_float2(rk, rk), make_float2(off, off));
+                if (!CLEAN) {
+                  y[i].x = x.x == -INFINITY ? -INFINITY : y[i].x;
+                  y[i].y = x.y == -INFINITY ? -INFINITY : y[i].y;
                 }
-                l_run = fmaf(sum.x + sum.y, f.z, l_run);
               }
-              tmem_st32u(tP + 32 * c, pk);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = half2_bits(y[i].x, y[i].y);
+              tmem_st16u(tS + 16 * c, pk);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const float2 *z = y + 8 * g;
+                const float2 s0 = __fadd2_rn(__fadd2_rn(z[0], z[1]), __fadd2_rn(z[2], z[3]));
+                const float2 s1 = __fadd2_rn(__fadd2_rn(z[4], z[5]), __fadd2_rn(z[6], z[7]));
+                const float2 sum = __fadd2_rn(s0, s1);
+                l_run = fmaf(sum.x + sum.y, fs[g].z, l_run);
+              }
             }
           };
           if ((t + 1) * BN <= all && sc[0].w != 0.f) tile(std::true_type{});
           else tile(std::false_type{});
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(b_p(half));
+          warp_arrive(b_p(half));
         }
         if (ok && !mbar_wait_warp(b_o(half), n_part & 1, a.wait_ns, abort_flag)) ok = false;
         ++n_part;
         if (!ok) break;
         tc_fence_after();
-      } else {
-        it += n;
+      }
+      it = it0 + n;
+      float ref = m_run == -INFINITY ? -INFINITY : m_run - C::kBias, f0 = 1.f, f1 = 0.f;
+      // ---- a block without a second half: half 0 adds half 1's part of the row to its own
+      const bool join = !two && n > 1;
+      if (join && half == 1) {
+        xch[r] = make_float2(ref, l_run);
+        tc_fence_before();
+        warp_arrive(b_j(1));
+      } else if (join) {
+        if (!mbar_wait_warp(b_j(1), n_join & 1, a.wait_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float2 g = xch[r];
+        const float mm = fmaxf(ref, g.x);
+        f0 = merge_factor(ref, l_run, mm);
+        f1 = merge_factor(g.x, g.y, mm);
+        l_run = fmaf(l_run, f0, g.y * f1);
+        ref = mm;
+      }
+      const bool has = n > 0 && (two || half == 0);    // an output to write that is not empty
+      if (!has) {
+        ref = -INFINITY;
+        l_run = 0.f;
       }
       // ---------------------------------------------------------------- epilogue
-      const float ref = m_run == -INFINITY ? -INFINITY : m_run - C::kBias;
+      auto load_o = [&](int cc, float (&o)[32]) {
+        tmem_ld32(tO + cc * 32, o);
+        if (join) {
+          float o1[32];
+          tmem_ld32(tO + D + cc * 32, o1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], f1, o[i] * f0);
+        } else {
+          tmem_wait_ld();
+        }
+      };
       if (sg.whole) {
         const float inv = l_run == 0.f ? 0.f : 1.f / l_run;      // a row that sees nothing is 0
+        const size_t at = orow < sa.n_rows ? address(orow) : 0;
 #pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           float o[32];
-          if (active) {
-            tmem_ld32(tO + cc * 32, o);
-            tmem_wait_ld();
+          if (has) {
+            load_o(cc, o);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0.f;
           }
-          if (row < sa.n_rows) {
+          if (orow < sa.n_rows) {
             uint4 *op = reinterpret_cast<uint4 *>(a.O + at * D + cc * 32);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -583,23 +682,22 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           }
           __syncwarp();
         }
-        if (a.lse && row < sa.n_rows)
+        if (a.lse && orow < sa.n_rows)
           a.lse[at] = l_run == 0.f ? -INFINITY : (ref + log2f(l_run)) * 0.6931471805599453f;
       } else {
         const size_t slot = (2 * static_cast<size_t>(cta) + (sg.first ? 1 : 0)) * C::ROWS + half * C::BM + r;
         a.m.ml[slot] = make_float2(ref, l_run);
-        if (active) {
+        if (has) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             float o[32];
-            tmem_ld32(tO + cc * 32, o);
-            tmem_wait_ld();
+            load_o(cc, o);
             float4 *op = reinterpret_cast<float4 *>(a.m.o + slot * D + cc * 32);
 #pragma unroll
             for (int u = 0; u < 8; ++u) op[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
           }
         }
-        if (tid == 0 && sg.first) {
+        if (tid == C::SOFTMAX_WARP * 32 && sg.first) {
           MergeItem mi;
           mi.b = sg.b;
           mi.h = sg.h;
@@ -607,6 +705,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           mi.go_on = sg.go_on;
           a.m.items[cta] = mi;
         }
+      }
+      if (join) {
+        if (half == 0) {
+          tc_fence_before();
+          warp_arrive(b_j(0));
+        } else if (!mbar_wait_warp(b_j(0), n_join & 1, a.wait_ns, abort_flag)) {   // half 0 has read O1
+          ok = false;
+          break;
+        }
+        ++n_join;
       }
       tc_fence_before();   // O is read before the next part's first P is published
     }
