@@ -462,9 +462,8 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
  * A row that sees nothing gives zeros, and -inf in lse.  Weights and products:
  * fp32 sums and statistics of exact 8-bit numbers and 16-bit weights.
  * workspace: 16-byte aligned device memory of the size that the first function
- *   gives for the same arguments on the current device (0: none needed), this
- *   call's own until it has run on its stream; nothing in it matters before or
- *   after.
+ *   gives for the same cache, Hq and Nq (0: none needed), this call's own until
+ *   it has run on its stream; nothing in it matters before or after.
  * Nq == 0 is a no-op.  Repeats bit for bit.  Asynchronous.
  */
 size_t mcs_cache_attention_workspace_size(const mcs_cache *cache, int Hq, int Nq);

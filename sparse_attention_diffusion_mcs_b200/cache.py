@@ -17,8 +17,8 @@ from typing import Optional, Tuple
 import torch
 
 from . import api
-from ._lib import McsCache, check, lib
-from .rotary import Rotary, _check_rotary, _position_strides
+from ._lib import McsCache, lib
+from .rotary import Rotary, _check_rotary, _position_strides, _run
 
 _I64x3 = ctypes.c_int64 * 3
 
@@ -50,6 +50,7 @@ class KVCache:
         self.n_pages, self.max_pages, self.device = n_pages, max_pages, dev
         self._c = McsCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                            page_table.data_ptr(), n_pages, max_pages, B, H, page, d)
+        self._ref = ctypes.byref(self._c)
 
     @property
     def capacity(self) -> int:
@@ -84,6 +85,14 @@ def _check_cache(cache: KVCache):
         raise ValueError("the cache must be on a CUDA device")
 
 
+def _row_strides(t: torch.Tensor, name: str):
+    """t's strides over B, H and n, with rows that can be read 16 bytes at a time."""
+    (b, h, n, _), (sb, sh, sn, sd) = t.shape, t.stride()
+    if sd != 1 or t.data_ptr() % 16 or (sb % 8 and b > 1) or (sh % 8 and h > 1) or (sn % 8 and n > 1):
+        raise ValueError(f"{name}'s rows must be contiguous and start on 16-byte boundaries")
+    return _I64x3(sb, sh, sn)
+
+
 def cache_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, start: torch.Tensor,
                  counts: Optional[torch.Tensor] = None, rotary: Optional[Rotary] = None,
                  positions: Optional[torch.Tensor] = None) -> None:
@@ -103,12 +112,7 @@ def cache_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, start: torch.
         raise ValueError(f"K and V must be [{cache.B}, {cache.H}, n, {cache.d}], got {tuple(K.shape)} and {tuple(V.shape)}")
     if n == 0:
         return
-    strides = []
-    for t, name in ((K, "K"), (V, "V")):
-        s = t.stride()
-        if s[3] != 1 or t.data_ptr() % 16 or any(x % 8 for x, m in zip(s, t.shape[:3]) if m > 1):
-            raise ValueError(f"{name}'s rows must be contiguous and start on 16-byte boundaries")
-        strides.append(_I64x3(*s[:3]))
+    ks, vs = _row_strides(K, "K"), _row_strides(V, "V")
     if start is None:
         raise TypeError("start must be a tensor")
     at = _per_sequence(start, "start", cache)
@@ -123,12 +127,11 @@ def cache_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, start: torch.
             pos = positions.data_ptr()
         elif len(rotary.axes) != 1:
             raise ValueError("several position axes need `positions`")
-        rot = ctypes.byref(rotary._c)
+        rot = rotary._ref
     elif positions is not None:
         raise ValueError("positions without rotary")
-    with api._on(cache.device):
-        check(lib().mcs_cache_append(ctypes.byref(cache._c), K.data_ptr(), V.data_ptr(), strides[0], strides[1], n, at,
-                                     how_many, pos, pos_b, pos_n, rot, api._stream(cache.device)), "mcs_cache_append")
+    _run("mcs_cache_append", cache.device, cache._ref, K.data_ptr(), V.data_ptr(), ks, vs, n, at, how_many, pos, pos_b, pos_n,
+         rot)
 
 
 def cache_read(cache: KVCache, start: torch.Tensor, n: int,
@@ -145,9 +148,7 @@ def cache_read(cache: KVCache, start: torch.Tensor, n: int,
     how_many = _per_sequence(counts, "counts", cache)
     K = torch.empty((cache.B, cache.H, n, cache.d), dtype=torch.bfloat16, device=cache.device)
     V = torch.empty_like(K)
-    with api._on(cache.device):
-        check(lib().mcs_cache_read(ctypes.byref(cache._c), at, how_many, n, K.data_ptr(), V.data_ptr(),
-                                   api._stream(cache.device)), "mcs_cache_read")
+    _run("mcs_cache_read", cache.device, cache._ref, at, how_many, n, K.data_ptr(), V.data_ptr())
     return K, V
 
 
@@ -178,11 +179,8 @@ def cache_attention(Q: torch.Tensor, cache: KVCache, lengths: torch.Tensor, caus
     else:
         api._check_tensor(out, "out", Q.shape, torch.bfloat16, cache.device)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=cache.device) if return_lse else None
-    with api._on(cache.device):
-        need = lib().mcs_cache_attention_workspace_size(ctypes.byref(cache._c), Hq, Nq)
-        ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
-        check(lib().mcs_cache_attention(ctypes.byref(cache._c), Q.data_ptr(), Hq, Nq, kept, how_many, int(causal),
-                                        api._scale(d, scale), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-                                        0 if ws is None else ws.data_ptr(), need, api._stream(cache.device)),
-              "mcs_cache_attention")
+    need = lib().mcs_cache_attention_workspace_size(cache._ref, Hq, Nq)
+    ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    _run("mcs_cache_attention", cache.device, cache._ref, Q.data_ptr(), Hq, Nq, kept, how_many, int(causal),
+         api._scale(d, scale), out.data_ptr(), 0 if lse is None else lse.data_ptr(), 0 if ws is None else ws.data_ptr(), need)
     return (out, lse) if return_lse else out

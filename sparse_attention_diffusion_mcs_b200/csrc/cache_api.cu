@@ -18,35 +18,24 @@ using namespace mcs;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 mcs_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MCS_OK : MCS_ERR_CUDA; }
 cudaStream_t cu(mcs_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
-struct Device {
-  int id = -1, sms = 0;
-};
-// the current device and its number of SMs (asked once per device)
-bool current_device(Device *d) {
-  static std::atomic<int> sms[kMaxDevices];
-  if (cudaGetDevice(&d->id) != cudaSuccess || d->id < 0 || d->id >= kMaxDevices) return false;
-  d->sms = sms[d->id].load(std::memory_order_relaxed);
-  if (!d->sms) {
-    if (cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess) return false;
-    sms[d->id].store(d->sms, std::memory_order_relaxed);
-  }
-  return true;
-}
+constexpr int kSms = 148;   // of a B200: the grids are sized for it, no result depends on it
 
-// a kernel's dynamic shared memory limit, set once per device
+// a kernel's dynamic shared memory limit (and clusters of more than 8 CTAs), set once per device
 template <auto *Kernel>
-cudaError_t allow_smem(const Device &d, int bytes) {
+cudaError_t allow_smem(int bytes, bool clusters = false) {
   static std::atomic<unsigned long long> done{0};
-  const unsigned long long bit = 1ull << d.id;
+  int dev = 0;
+  const cudaError_t ge = cudaGetDevice(&dev);
+  if (ge != cudaSuccess) return ge;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -95,14 +84,14 @@ mcs_status check_cache(const mcs_cache *c, CacheView *v) {
 
 // ---------------------------------------------------------------- rotate
 template <typename T>
-cudaError_t launch_rotate(RotateArgs &a, bool vec, const Device &dev, cudaStream_t s) {
+cudaError_t launch_rotate(RotateArgs &a, bool vec, cudaStream_t s) {
   const long long per_token = vec ? a.d / 16 : a.d - a.t.pairs;
   const long long threads = static_cast<long long>(a.B) * a.N * per_token;
   const long long blocks = (threads + kRotateThreads - 1) / kRotateThreads;
   // A thread walks over a group of heads with one set of angles.  Few tokens:
-  // smaller groups, down to one head, until the grid has 1024 threads per SM.
-  const long long want = 1024ll * dev.sms / kRotateThreads;
-  long long groups = (want + blocks - 1) / blocks;
+  // smaller groups, down to one head, until the SMs have a CTA each.  (16 heads,
+  // 16382 tokens: one group 15.4 us, three 17.5, eight 24.4.)
+  long long groups = (kSms + blocks - 1) / blocks;
   groups = groups < 1 ? 1 : (groups > a.H ? a.H : groups);
   a.heads = static_cast<int>((a.H + groups - 1) / groups);
   const dim3 grid(static_cast<unsigned>(blocks), (a.H + a.heads - 1) / a.heads);
@@ -114,50 +103,54 @@ cudaError_t launch_rotate(RotateArgs &a, bool vec, const Device &dev, cudaStream
 }
 
 // ---------------------------------------------------------------- attention over the cache
-// CTAs that deal the work of one call among themselves, at most (two on each SM)
-constexpr int kMaxCtas = 2 * 148;
-
 // sizes of one call: blocks of rows, and how they are computed
 struct AttnPlan {
-  int mt;                        // row tiles of 16 of a block (cache_rows_kernel); 0: cache_tile_kernel
-  int rows;                      // rows of a block
+  bool rows;                     // cache_rows_kernel (blocks of 16 rows), else cache_tile_kernel (256)
+  int block;                     // rows of a block
   int ctas;                      // CTAs that share the work; 0: clusters, no workspace
   int split;                     // CTAs of a cluster
 };
-AttnPlan plan_attention(const CacheView &c, int B, long long n_rows, int sms) {
+// By sizes known here (the table's places; lengths are not):
+// - Little work: clusters of 16 CTAs at most, as many as fill the SMs once and
+//   as there can be tiles, on blocks of 16 rows.  More rows than 16 read the
+//   keys once a block, but start at once: 20 rows of 16 heads against 8191
+//   tokens took 26 us as one block of 32, 25 with the tile kernel and 5 of merge.
+// - Else 16 rows or fewer are bound by reading the keys (cache_rows_kernel: 16 rows
+//   of 64 heads, 819200 tokens, 294 us; the tile kernel 467), more by the products
+//   (32 rows: the tile kernel 467, blocks of 32 rows 1276).
+AttnPlan plan_attention(const CacheView &c, int B, long long n_rows) {
   AttnPlan p;
-  p.mt = n_rows <= 16 ? 1 : n_rows <= 32 ? 2 : 0;
-  p.rows = p.mt ? 16 * p.mt : 256;
-  const long long blocks = (n_rows + p.rows - 1) / p.rows;
-  const long long items = static_cast<long long>(B) * c.H * blocks;
   const long long tiles = (static_cast<long long>(c.max_pages) * c.page + kKeyTile - 1) / kKeyTile;
-  const int resident = sms * (p.mt == 1 ? 2 : 1);
-  p.ctas = resident < kMaxCtas ? resident : kMaxCtas;
+  const long long items = static_cast<long long>(B) * c.H * ((n_rows + 15) / 16);
+  p.rows = true;
+  p.block = 16;
+  p.ctas = 2 * kSms;
   p.split = 1;
-  // Little work (by the table's places; lengths are not known here): clusters
-  // of 8 CTAs (the portable size) at most, as many as fill the SMs once and as
-  // there can be tiles.
-  if (p.mt && tiles <= 64 && items * tiles <= 16ll * sms) {
-    long long split = resident / items;
-    split = split > 8 ? 8 : split;
+  if (tiles <= 64 && items * tiles <= 16ll * kSms) {
+    long long split = p.ctas / items;
+    split = split > 16 ? 16 : split;
     split = split > tiles ? tiles : split;
     p.split = static_cast<int>(split < 1 ? 1 : split);
     p.ctas = 0;
+  } else if (n_rows > 16) {
+    p.rows = false;
+    p.block = 256;
+    p.ctas = kSms;
   }
   return p;
 }
 
-template <int D, int MT>
-cudaError_t launch_rows(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, cudaStream_t s) {
-  using C = RowsCfg<D, MT>;
-  static_assert(C::SMEM * (MT == 1 ? 2 : 1) + (MT == 1 ? 2048 : 0) <= 232448, "shared memory budget");
+template <int D>
+cudaError_t launch_rows(CacheAttnArgs &a, const AttnPlan &p, cudaStream_t s) {
+  using C = RowsCfg<D>;
+  static_assert(2 * (C::SMEM + 1024) <= 233472, "two CTAs on an SM");
   if (p.ctas) {
-    cudaError_t e = allow_smem<cache_rows_kernel<D, MT, false>>(dev, C::SMEM);
+    const cudaError_t e = allow_smem<cache_rows_kernel<D, false>>(C::SMEM);
     if (e != cudaSuccess) return e;
-    cache_rows_kernel<D, MT, false><<<p.ctas, C::THREADS, C::SMEM, s>>>(a);
+    cache_rows_kernel<D, false><<<p.ctas, C::THREADS, C::SMEM, s>>>(a);
     return cudaGetLastError();
   }
-  cudaError_t e = allow_smem<cache_rows_kernel<D, MT, true>>(dev, C::SMEM);
+  const cudaError_t e = allow_smem<cache_rows_kernel<D, true>>(C::SMEM, true);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.split), static_cast<unsigned>(a.s.B * a.s.H),
@@ -172,21 +165,21 @@ cudaError_t launch_rows(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, 
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<D, MT, true>, a);
+  return cudaLaunchKernelEx(&cfg, cache_rows_kernel<D, true>, a);
 }
 
 template <int D>
-cudaError_t launch_tile(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, cudaStream_t s) {
+cudaError_t launch_tile(CacheAttnArgs &a, const AttnPlan &p, cudaStream_t s) {
   using C = TileCfg<D>;
-  const cudaError_t e = allow_smem<cache_tile_kernel<D>>(dev, C::SMEM);
+  const cudaError_t e = allow_smem<cache_tile_kernel<D>>(C::SMEM);
   if (e != cudaSuccess) return e;
   cache_tile_kernel<D><<<p.ctas, C::THREADS, C::SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_attention(CacheAttnArgs &a, const AttnPlan &p, const Device &dev, cudaStream_t s) {
-  return p.mt == 1 ? launch_rows<D, 1>(a, p, dev, s) : p.mt == 2 ? launch_rows<D, 2>(a, p, dev, s) : launch_tile<D>(a, p, dev, s);
+cudaError_t launch_attention(CacheAttnArgs &a, const AttnPlan &p, cudaStream_t s) {
+  return p.rows ? launch_rows<D>(a, p, s) : launch_tile<D>(a, p, s);
 }
 
 template <int D>
@@ -200,9 +193,9 @@ cudaError_t launch_merge(const CacheAttnArgs &a, const AttnPlan &p, cudaStream_t
   m.Nq = a.s.Nq;
   m.share = a.s.share;
   m.n_rows = a.s.n_rows;
-  m.rows = p.rows;
+  m.rows = p.block;
   const int at_once = kMergeThreads / (D / 4);
-  cache_merge_kernel<D><<<dim3(p.ctas, (p.rows + at_once - 1) / at_once), kMergeThreads, 0, s>>>(m);
+  cache_merge_kernel<D><<<dim3(p.ctas, (p.block + at_once - 1) / at_once), kMergeThreads, 0, s>>>(m);
   return cudaGetLastError();
 }
 
@@ -243,11 +236,9 @@ mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, cons
   // 16-byte vectors need whole units of 16 numbers and aligned rows
   const bool vec = d % 16 == 0 && (a.t.interleaved || a.t.pairs % 8 == 0) && aligned16(x) && aligned16(out) &&
                    a.sb * elt % 16 == 0 && a.sh * elt % 16 == 0 && a.sn * elt % 16 == 0;
-  Device dev;
-  if (!current_device(&dev)) return MCS_ERR_CUDA;
-  const cudaError_t e = dtype == MCS_FP32   ? launch_rotate<float>(a, vec, dev, cu(stream))
-                        : dtype == MCS_FP16 ? launch_rotate<__half>(a, vec, dev, cu(stream))
-                                            : launch_rotate<bf16>(a, vec, dev, cu(stream));
+  const cudaError_t e = dtype == MCS_FP32   ? launch_rotate<float>(a, vec, cu(stream))
+                        : dtype == MCS_FP16 ? launch_rotate<__half>(a, vec, cu(stream))
+                                            : launch_rotate<bf16>(a, vec, cu(stream));
   return cuda_status(e);
 }
 
@@ -290,12 +281,11 @@ mcs_status mcs_cache_append(const mcs_cache *cache, const void *K, const void *V
   // n tokens reach into ceil((n - 1) / page) + 1 pages at most
   const dim3 grid((n + a.c.page - 2) / a.c.page + 1, a.c.H, cache->B);
   const int units = a.c.page * (a.c.d / 16);
+  const int threads = units < kAppendThreads ? units : kAppendThreads;
   if (units <= kAppendThreads)
-    append_kernel<1><<<grid, kAppendThreads, 0, cu(stream)>>>(a);
-  else if (units <= 2 * kAppendThreads)
-    append_kernel<2><<<grid, kAppendThreads, 0, cu(stream)>>>(a);
+    append_kernel<1><<<grid, threads, 0, cu(stream)>>>(a);
   else
-    append_kernel<4><<<grid, kAppendThreads, 0, cu(stream)>>>(a);
+    append_kernel<2><<<grid, threads, 0, cu(stream)>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
@@ -314,22 +304,23 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
   a.K = static_cast<bf16 *>(K);
   a.V = static_cast<bf16 *>(V);
   a.n = n;
-  a.units = static_cast<long long>(cache->B) * a.c.H * n * (a.c.d / 16);
-  const long long blocks = (a.units + kReadThreads - 1) / kReadThreads;
+  a.page_shift = a.c.page == 16 ? 4 : a.c.page == 32 ? 5 : a.c.page == 64 ? 6 : 7;
+  const long long units = static_cast<long long>(n) * (a.c.d / 16);
+  const int threads = units < kReadThreads ? static_cast<int>((units + 31) / 32 * 32) : kReadThreads;
+  const long long blocks = (units + threads - 1) / threads;
   if (blocks > INT_MAX) return MCS_ERR_INVALID_ARG;
   if (!(a.status = device_status_word())) return MCS_ERR_CUDA;
-  cache_read_kernel<<<static_cast<unsigned>(blocks), kReadThreads, 0, cu(stream)>>>(a);
+  cache_read_kernel<<<dim3(static_cast<unsigned>(blocks), a.c.H, cache->B), threads, 0, cu(stream)>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
 size_t mcs_cache_attention_workspace_size(const mcs_cache *cache, int Hq, int Nq) {
   CacheView c;
-  Device dev;
   if (check_cache(cache, &c) != MCS_OK || Hq < 1 || Hq % c.H != 0 || Nq < 0) return 0;
   const long long n_rows = static_cast<long long>(Nq) * (Hq / c.H);
-  if (n_rows == 0 || n_rows > (1 << 20) || !current_device(&dev)) return 0;
-  const AttnPlan p = plan_attention(c, cache->B, n_rows, dev.sms);
-  return p.ctas ? merge_space(p.ctas, p.rows, c.d, nullptr, nullptr) : 0;
+  if (n_rows == 0 || n_rows > (1 << 20)) return 0;
+  const AttnPlan p = plan_attention(c, cache->B, n_rows);
+  return p.ctas ? merge_space(p.ctas, p.block, c.d, nullptr, nullptr) : 0;
 }
 
 mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, int Nq, const int32_t *lengths,
@@ -347,12 +338,11 @@ mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, in
   const long long n_rows = static_cast<long long>(Nq) * (Hq / a.c.H);
   if (n_rows > (1 << 20)) return MCS_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return MCS_ERR_INVALID_ARG;
-  Device dev;
-  if (!current_device(&dev) || !(a.status = device_status_word())) return MCS_ERR_CUDA;
-  const AttnPlan p = plan_attention(a.c, cache->B, n_rows, dev.sms);
+  if (!(a.status = device_status_word())) return MCS_ERR_CUDA;
+  const AttnPlan p = plan_attention(a.c, cache->B, n_rows);
   if (p.ctas) {
-    if (!workspace || workspace_bytes < merge_space(p.ctas, p.rows, a.c.d, nullptr, nullptr)) return MCS_ERR_WORKSPACE;
-    merge_space(p.ctas, p.rows, a.c.d, workspace, &a.m);
+    if (!workspace || workspace_bytes < merge_space(p.ctas, p.block, a.c.d, nullptr, nullptr)) return MCS_ERR_WORKSPACE;
+    merge_space(p.ctas, p.block, a.c.d, workspace, &a.m);
   }
   a.Q = static_cast<const bf16 *>(Q);
   a.O = static_cast<bf16 *>(O);
@@ -366,13 +356,13 @@ mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, in
   a.s.causal = causal != 0;
   a.s.cap = a.c.max_pages * a.c.page;
   a.s.n_rows = static_cast<int>(n_rows);
-  a.s.n_blocks = static_cast<int>((n_rows + p.rows - 1) / p.rows);
+  a.s.n_blocks = static_cast<int>((n_rows + p.block - 1) / p.block);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = wait_limit_ns();
   const size_t rows = static_cast<size_t>(a.c.n_pages) * a.c.H * a.c.page;
   if (!map_byte_rows(&a.tmK, a.c.k, a.c.d, rows, a.c.page) || !map_byte_rows(&a.tmV, a.c.v, a.c.d, rows, a.c.page))
     return MCS_ERR_CUDA;
-  cudaError_t e = a.c.d == 64 ? launch_attention<64>(a, p, dev, cu(stream)) : launch_attention<128>(a, p, dev, cu(stream));
+  cudaError_t e = a.c.d == 64 ? launch_attention<64>(a, p, cu(stream)) : launch_attention<128>(a, p, cu(stream));
   if (e == cudaSuccess && p.ctas) e = a.c.d == 64 ? launch_merge<64>(a, p, cu(stream)) : launch_merge<128>(a, p, cu(stream));
   return cuda_status(e);
 }

@@ -14,7 +14,7 @@
 // largest magnitude: exact for bf16 numbers down to 2^-17 of it, and off by
 // 2^-25 of it below.
 //
-// A CTA takes 16 MT rows -- all query heads that share a key head, times their
+// A CTA takes 16 rows -- all query heads that share a key head, times their
 // tokens -- and runs of 128-key tiles, dealt in one of two ways.  Little work:
 // a cluster of CTAs takes one item (cache_sched.cuh), each its share of the
 // tiles, and merges (m, l, O) through distributed shared memory, in one launch.
@@ -51,25 +51,25 @@ struct CacheAttnArgs {
   unsigned long long wait_ns;
 };
 
-template <int D, int MT>
+template <int D>
 struct RowsCfg {
   static constexpr int BN = 128;                       // keys per tile
   static constexpr int TILE = BN * D;                  // bytes of a K or V tile
-  static constexpr int NS = (D == 128 ? 3 : 6) * (MT == 1 ? 1 : 2);
+  static constexpr int NS = (D == 128 ? 3 : 6);
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_SC = OFF_KV + NS * 2 * TILE;   // per stage: 8 x float4 (ks, log2 vs, 1 / vs, -)
   static constexpr int OFF_BAR = OFF_SC + NS * 8 * 16;
   static constexpr int OFF_MISC = OFF_BAR + 16 * NS;
-  static constexpr int OFF_ML = OFF_MISC + 16;            // merged (reference, l) of 16 MT rows
-  static constexpr int OFF_WML = OFF_ML + 16 * MT * 8;    // per warp (reference, l)
+  static constexpr int OFF_ML = OFF_MISC + 16;            // merged (reference, l) of 16 rows
+  static constexpr int OFF_WML = OFF_ML + 16 * 8;    // per warp (reference, l)
   // the warps' O on its way into the CTA's, 32 numbers of a row at a time
   static constexpr int OLD = 32 + 4;
-  static constexpr int OFF_WO = OFF_WML + 4 * 16 * MT * 8;
-  static constexpr int SMEM = OFF_WO + 4 * 16 * MT * OLD * 4 + 1024;
+  static constexpr int OFF_WO = OFF_WML + 4 * 16 * 8;
+  static constexpr int SMEM = OFF_WO + 4 * 16 * OLD * 4 + 1024;
   // clusters, after their only run of tiles, over the ring: the CTA's O
   static constexpr int OFF_O = 0;
   static_assert(OFF_WML % 16 == 0 && OFF_WO % 16 == 0, "16-byte aligned");
-  static_assert(16 * MT * D * 4 <= OFF_SC, "a cluster's O fits the ring");
+  static_assert(16 * D * 4 <= OFF_SC, "a cluster's O fits the ring");
   static constexpr int THREADS = 5 * 32;
 };
 
@@ -132,11 +132,11 @@ __device__ __forceinline__ void cluster_sync() {
 // weights are held times 2^kBias in fp16
 constexpr float kRowsBias = 14.f;
 
-template <int D, int MT, bool CLUSTER>
-__global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
+template <int D, bool CLUSTER>
+__global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
     cache_rows_kernel(const __grid_constant__ CacheAttnArgs a) {
-  using C = RowsCfg<D, MT>;
-  using S = Sched<16 * MT, false>;
+  using C = RowsCfg<D>;
+  using S = Sched<16, false>;
   constexpr int NS = C::NS, BN = C::BN, SEG = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     bool ok = true;
     int it = 0;
     while (next(sg)) {
-    const int row0 = sg.block * 16 * MT;                 // rows are (token, query head of the group)
+    const int row0 = sg.block * 16;                 // rows are (token, query head of the group)
     const int kmax = sg.kmax;
     // keys that row i of the item sees: [0, limit)
     auto limit_of = [&](int row) {
@@ -288,68 +288,63 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
       if (row >= sa.n_rows || i >= sg.nq) return 0;
       return sa.causal ? max(sg.len - sg.nq + i + 1, 0) : sg.len;
     };
-    const int last_row = min(row0 + 16 * MT, sa.n_rows) - 1;
-    uint32_t qa[MT][SEG][4][4];
-    float rowf[MT][2];
-    int lim[MT][2];
+    const int last_row = min(row0 + 16, sa.n_rows) - 1;
+    uint32_t qa[SEG][4][4];
+    float rowf[2];
+    int lim[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int u = 0; u < 2; ++u) {
+      const int row = row0 + u * 8 + g;
+      lim[u] = limit_of(row);
+      uint4 w[SEG][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int row = row0 + mt * 16 + u * 8 + g;
-        lim[mt][u] = limit_of(row);
-        uint4 w[SEG][2];
-#pragma unroll
-        for (int sgm = 0; sgm < SEG; ++sgm) w[sgm][0] = w[sgm][1] = make_uint4(0, 0, 0, 0);
-        if (row < sa.n_rows) {
-          const int i = row / share, hq = sg.h * share + row % share;
-          const uint4 *q = reinterpret_cast<const uint4 *>(
-              a.Q + ((static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i) * D);
-#pragma unroll
-          for (int sgm = 0; sgm < SEG; ++sgm) {
-            w[sgm][0] = q[sgm * 8 + 2 * t];
-            w[sgm][1] = q[sgm * 8 + 2 * t + 1];
-          }
-        }
-        // the row's largest magnitude, as bf16 bits
-        uint32_t am = 0;
-        const uint32_t *x = reinterpret_cast<const uint32_t *>(w);
-#pragma unroll
-        for (int i = 0; i < SEG * 8; ++i) am = max(am, max((x[i] << 1) & 0xFFFEu, (x[i] >> 15) & 0xFFFEu));
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        rowf[mt][u] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        if (am >> 8 == 255) rowf[mt][u] = __uint_as_float(0x7FC00000u);   // a query that is not finite: NaN
+      for (int sgm = 0; sgm < SEG; ++sgm) w[sgm][0] = w[sgm][1] = make_uint4(0, 0, 0, 0);
+      if (row < sa.n_rows) {
+        const int i = row / share, hq = sg.h * share + row % share;
+        const uint4 *q = reinterpret_cast<const uint4 *>(
+            a.Q + ((static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i) * D);
 #pragma unroll
         for (int sgm = 0; sgm < SEG; ++sgm) {
-          const uint32_t *y = reinterpret_cast<const uint32_t *>(w[sgm]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint32_t z = y[2 * j + p];
-              qa[mt][sgm][j][u + 2 * p] =
-                  half2_bits(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
-            }
+          w[sgm][0] = q[sgm * 8 + 2 * t];
+          w[sgm][1] = q[sgm * 8 + 2 * t + 1];
         }
       }
+      // the row's largest magnitude, as bf16 bits
+      uint32_t am = 0;
+      const uint32_t *x = reinterpret_cast<const uint32_t *>(w);
+#pragma unroll
+      for (int i = 0; i < SEG * 8; ++i) am = max(am, max((x[i] << 1) & 0xFFFEu, (x[i] >> 15) & 0xFFFEu));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      rowf[u] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      if (am >> 8 == 255) rowf[u] = __uint_as_float(0x7FC00000u);   // a query that is not finite: NaN
+#pragma unroll
+      for (int sgm = 0; sgm < SEG; ++sgm) {
+        const uint32_t *y = reinterpret_cast<const uint32_t *>(w[sgm]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t z = y[2 * j + p];
+            qa[sgm][j][u + 2 * p] =
+                half2_bits(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
+          }
+      }
+    }
     // keys every row of the CTA sees: no row of a block sees fewer than its first (queries behind nq: none)
     const int all = min(limit_of(row0), limit_of(last_row));
 
     constexpr int NT = D / 8;          // column tiles of O
-    float o[MT][NT][4];
-    float m[MT][2], l[MT][2];
+    float o[NT][4];
+    float m[2], l[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int c = 0; c < NT; ++c)
 #pragma unroll
-      for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][c][e] = 0.f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
     for (int tt = sg.t0; tt < sg.t1; ++tt, ++it) {
       const int s = it % NS;
       if (!mbar_wait_warp(b_full(s), (it / NS) & 1, a.wait_ns, abort_flag)) {
@@ -368,13 +363,11 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
         const float4 sc0 = scp[0], sc1 = scp[1];
         const bool clean = key0 + 32 <= all && sc0.y > -INFINITY && sc1.y > -INFINITY;
         // ---- scores of 32 keys
-        float sc[MT][4][4];
+        float sc[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][i][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
           const int r = 8 * i + key_of<D>(g);
 #pragma unroll
           for (int sgm = 0; sgm < SEG; ++sgm) {
@@ -384,66 +377,61 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint32_t b0 = half2_of_e4m3x2(x[j]), b1 = half2_of_e4m3x2_hi(x[j]);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma_f16(sc[mt][i], qa[mt][sgm][j][0], qa[mt][sgm][j][1], qa[mt][sgm][j][2], qa[mt][sgm][j][3], b0, b1);
+              mma_f16(sc[i], qa[sgm][j][0], qa[sgm][j][1], qa[sgm][j][2], qa[sgm][j][3], b0, b1);
             }
           }
         }
         // ---- online softmax; column 2t + u of group i is key key0 + 8 i + key_of(2t + u)
-        uint32_t pa[MT][4][2];
+        uint32_t pa[4][2];
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float mx[2] = {-INFINITY, -INFINITY};
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = i < 2 ? sc0 : sc1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 f = i < 2 ? sc0 : sc1;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float y = fmaf(sc[mt][i][e], rowf[mt][e >> 1] * f.x, f.y);
-              if (!clean) {
-                const int key = key0 + 8 * i + key_of<D>(2 * t + (e & 1));
-                y = key < lim[mt][e >> 1] && f.y > -INFINITY ? y : -INFINITY;
-              }
-              sc[mt][i][e] = y;
-              mx[e >> 1] = fmaxf(mx[e >> 1], y);
+          for (int e = 0; e < 4; ++e) {
+            float y = fmaf(sc[i][e], rowf[e >> 1] * f.x, f.y);
+            if (!clean) {
+              const int key = key0 + 8 * i + key_of<D>(2 * t + (e & 1));
+              y = key < lim[e >> 1] && f.y > -INFINITY ? y : -INFINITY;
             }
+            sc[i][e] = y;
+            mx[e >> 1] = fmaxf(mx[e >> 1], y);
           }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+          mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+          float al[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-            mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+            const float nm = fmaxf(m[u], mx[u]);
+            al[u] = nm == m[u] ? 1.f : ex2_approx(m[u] - nm);
+            m[u] = nm;
+            l[u] *= al[u];
           }
-          if (__any_sync(0xffffffffu, mx[0] > m[mt][0] || mx[1] > m[mt][1])) {
-            float al[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float nm = fmaxf(m[mt][u], mx[u]);
-              al[u] = nm == m[mt][u] ? 1.f : ex2_approx(m[mt][u] - nm);
-              m[mt][u] = nm;
-              l[mt][u] *= al[u];
-            }
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-              o[mt][c][0] *= al[0];
-              o[mt][c][1] *= al[0];
-              o[mt][c][2] *= al[1];
-              o[mt][c][3] *= al[1];
-            }
+          for (int c = 0; c < NT; ++c) {
+            o[c][0] *= al[0];
+            o[c][1] *= al[0];
+            o[c][2] *= al[1];
+            o[c][3] *= al[1];
           }
-          const float mu[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kRowsBias,
-                               m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kRowsBias};
+        }
+        const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0] - kRowsBias,
+                             m[1] == -INFINITY ? 0.f : m[1] - kRowsBias};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float inv = i < 2 ? sc0.z : sc1.z;
-            float p[4];
+        for (int i = 0; i < 4; ++i) {
+          const float inv = i < 2 ? sc0.z : sc1.z;
+          float p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = ex2_approx(sc[mt][i][e] - mu[e >> 1]);
-            l[mt][0] = fmaf(p[0] + p[1], inv, l[mt][0]);
-            l[mt][1] = fmaf(p[2] + p[3], inv, l[mt][1]);
-            pa[mt][i][0] = half2_bits(p[0], p[1]);
-            pa[mt][i][1] = half2_bits(p[2], p[3]);
-          }
+          for (int e = 0; e < 4; ++e) p[e] = ex2_approx(sc[i][e] - mu[e >> 1]);
+          l[0] = fmaf(p[0] + p[1], inv, l[0]);
+          l[1] = fmaf(p[2] + p[3], inv, l[1]);
+          pa[i][0] = half2_bits(p[0], p[1]);
+          pa[i][1] = half2_bits(p[2], p[3]);
         }
         // ---- P.V; column g of tile c is number (D / 8) g + c
 #pragma unroll
@@ -472,10 +460,7 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
             const uint32_t b1[4] = {half2_of_e4m3x2(hi0), half2_of_e4m3x2_hi(hi0), half2_of_e4m3x2(hi1), half2_of_e4m3x2_hi(hi1)};
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma_f16(o[mt][4 * q + c], pa[mt][2 * ii][0], pa[mt][2 * ii][1], pa[mt][2 * ii + 1][0], pa[mt][2 * ii + 1][1],
-                        b0[c], b1[c]);
+              mma_f16(o[4 * q + c], pa[2 * ii][0], pa[2 * ii][1], pa[2 * ii + 1][0], pa[2 * ii + 1][1], b0[c], b1[c]);
           }
         }
       }
@@ -487,35 +472,30 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     float2 *wml = reinterpret_cast<float2 *>(smem + C::OFF_WML);
     float *wo = reinterpret_cast<float *>(smem + C::OFF_WO);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float s = l[mt][u];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if (t == 0)
-          wml[warp * 16 * MT + mt * 16 + u * 8 + g] =
-              make_float2(m[mt][u] == -INFINITY ? -INFINITY : m[mt][u] - kRowsBias, s);
-      }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    // this thread merges 4 numbers of row tid / 8 (and 16 rows on, for the second row tile)
-    float2 ml[MT];
-    float f[MT][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = mt * 16 + tid / 8;
-      float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, wml[w * 16 * MT + r].x);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 p = wml[w * 16 * MT + r];
-        f[mt][w] = merge_factor(p.x, p.y, mm);
-        ll = fmaf(p.y, f[mt][w], ll);
-      }
-      ml[mt] = make_float2(mm, ll);
+    for (int u = 0; u < 2; ++u) {
+      float s = l[u];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (t == 0)
+        wml[warp * 16 + u * 8 + g] =
+            make_float2(m[u] == -INFINITY ? -INFINITY : m[u] - kRowsBias, s);
     }
-    const size_t slot = CLUSTER ? 0 : (2 * static_cast<size_t>(rank) + (sg.first ? 1 : 0)) * 16 * MT;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    // this thread merges 4 numbers of row r
+    float2 ml;
+    float f[4];
+    const int r = tid / 8;
+    float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mm = fmaxf(mm, wml[w * 16 + r].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 p = wml[w * 16 + r];
+      f[w] = merge_factor(p.x, p.y, mm);
+      ll = fmaf(p.y, f[w], ll);
+    }
+    ml = make_float2(mm, ll);
+    const size_t slot = CLUSTER ? 0 : (2 * static_cast<size_t>(rank) + (sg.first ? 1 : 0)) * 16;
     if constexpr (!CLUSTER) {
       if (tid == 0 && sg.first && !sg.whole && ok) {
         MergeItem mi;
@@ -528,50 +508,41 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     }
     float2 *cml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     float *oc = reinterpret_cast<float *>(smem + C::OFF_O);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = mt * 16 + tid / 8;
-      if (tid % 8 == 0) {
-        if constexpr (CLUSTER) cml[r] = ml[mt];
-        else if (!sg.whole) a.m.ml[slot + r] = ml[mt];
-      }
+    if (tid % 8 == 0) {
+      if constexpr (CLUSTER) cml[r] = ml;
+      else if (!sg.whole) a.m.ml[slot + r] = ml;
     }
 #pragma unroll
     for (int q = 0; q < NT / 4; ++q) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float4 *>(wo + (warp * 16 * MT + mt * 16 + u * 8 + g) * C::OLD + 4 * (2 * t + e)) =
-                make_float4(o[mt][4 * q][2 * u + e], o[mt][4 * q + 1][2 * u + e], o[mt][4 * q + 2][2 * u + e],
-                            o[mt][4 * q + 3][2 * u + e]);
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4 *>(wo + (warp * 16 + u * 8 + g) * C::OLD + 4 * (2 * t + e)) =
+              make_float4(o[4 * q][2 * u + e], o[4 * q + 1][2 * u + e], o[4 * q + 2][2 * u + e],
+                          o[4 * q + 3][2 * u + e]);
       asm volatile("bar.sync 1, 128;" ::: "memory");
+      const int te = tid % 8, col = NT * te + 4 * q;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int r = mt * 16 + tid / 8, te = tid % 8, col = NT * te + 4 * q;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 16 * MT + r) * C::OLD + 4 * te);
-          const float y = f[mt][w];
-          acc = make_float4(fmaf(x.x, y, acc.x), fmaf(x.y, y, acc.y), fmaf(x.z, y, acc.z), fmaf(x.w, y, acc.w));
-        }
-        if constexpr (CLUSTER) {
-          *reinterpret_cast<float4 *>(oc + r * D + col) = acc;
-        } else if (!sg.whole) {
-          *reinterpret_cast<float4 *>(a.m.o + (slot + r) * D + col) = acc;
-        } else if (row0 + r < sa.n_rows && ok) {
-          const float inv = ml[mt].y == 0.f ? 0.f : 1.f / ml[mt].y;      // a row that sees nothing is 0
-          const int row = row0 + r, i = row / share, hq = sg.h * share + row % share;
-          const size_t at = (static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i;
-          *reinterpret_cast<uint2 *>(a.O + at * D + col) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-          // l is in units of 2^reference: the sum of exp(score) is l 2^reference
-          if (a.lse && te == 0 && q == 0)
-            a.lse[at] = ml[mt].y == 0.f ? -INFINITY : (ml[mt].x + log2f(ml[mt].y)) * 0.6931471805599453f;
-        }
+      for (int w = 0; w < 4; ++w) {
+        const float4 x = *reinterpret_cast<const float4 *>(wo + (w * 16 + r) * C::OLD + 4 * te);
+        const float y = f[w];
+        acc = make_float4(fmaf(x.x, y, acc.x), fmaf(x.y, y, acc.y), fmaf(x.z, y, acc.z), fmaf(x.w, y, acc.w));
+      }
+      if constexpr (CLUSTER) {
+        *reinterpret_cast<float4 *>(oc + r * D + col) = acc;
+      } else if (!sg.whole) {
+        *reinterpret_cast<float4 *>(a.m.o + (slot + r) * D + col) = acc;
+      } else if (row0 + r < sa.n_rows && ok) {
+        const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;      // a row that sees nothing is 0
+        const int row = row0 + r, i = row / share, hq = sg.h * share + row % share;
+        const size_t at = (static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i;
+        *reinterpret_cast<uint2 *>(a.O + at * D + col) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        // l is in units of 2^reference: the sum of exp(score) is l 2^reference
+        if (a.lse && te == 0 && q == 0)
+          a.lse[at] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
       }
       if (q + 1 < NT / 4) asm volatile("bar.sync 1, 128;" ::: "memory");
     }
@@ -585,8 +556,8 @@ __global__ void __launch_bounds__(RowsCfg<D, MT>::THREADS, MT == 1 ? 2 : 1)
     else
       __syncthreads();
     if (!*abort_flag) {
-      const int row0 = run.block * 16 * MT;
-      const int rows_here = min(16 * MT, sa.n_rows - row0);
+      const int row0 = run.block * 16;
+      const int rows_here = min(16, sa.n_rows - row0);
       for (int idx = rank * C::THREADS + tid; idx < rows_here * (D / 4); idx += ranks * C::THREADS) {
         const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
         float mm = -INFINITY;

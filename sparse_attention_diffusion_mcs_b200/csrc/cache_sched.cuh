@@ -227,17 +227,31 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
   const int rows = min(a.rows, a.n_rows - row0);
   for (int r = blockIdx.y * RPC + threadIdx.x / TPR; r < rows; r += gridDim.y * RPC) {
     auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.rows + r; };
-    float mm = -INFINITY;
-    for (int k = 0; k <= it.go_on; ++k) mm = fmaxf(mm, a.m.ml[slot(k)].x);
+    // four parts at once, the first four (mostly all) before anything waits for them
+    float2 p[4];
+    float4 x[4];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const size_t at = slot(min(k0 + u, it.go_on));
+        p[u] = a.m.ml[at];
+        x[u] = *reinterpret_cast<const float4 *>(a.m.o + at * D + col);
+      }
+    };
+    load(0);
+    float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
+    for (int k = 4; k <= it.go_on; ++k) mm = fmaxf(mm, a.m.ml[slot(k)].x);
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k <= it.go_on; ++k) {
-      const float2 p = a.m.ml[slot(k)];
-      const float f = merge_factor(p.x, p.y, mm);
-      if (f != 0.f) {                                        // (NaN counts; a part without keys has no O)
-        const float4 x = *reinterpret_cast<const float4 *>(a.m.o + slot(k) * D + col);
-        l = fmaf(p.y, f, l);
-        acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+    for (int k0 = 0; k0 <= it.go_on; k0 += 4) {
+      if (k0) load(k0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = merge_factor(p[u].x, p[u].y, mm);
+        if (k0 + u <= it.go_on && f != 0.f) {                // (NaN counts; a part without keys has no O)
+          l = fmaf(p[u].y, f, l);
+          acc = make_float4(fmaf(x[u].x, f, acc.x), fmaf(x[u].y, f, acc.y), fmaf(x[u].z, f, acc.z), fmaf(x[u].w, f, acc.w));
+        }
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;

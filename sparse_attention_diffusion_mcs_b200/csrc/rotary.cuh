@@ -7,8 +7,9 @@
 // pos * F mod 2^64 is then the phase, exact for every 32-bit position (the
 // product wraps whole turns away; F's own rounding moves it by less than
 // pos * 2^-65 turns), so far positions lose nothing and no table of angles is
-// read.  The phase's top 32 bits, as a signed number of half turns, go to
-// sincospif: its rounding to fp32 costs at most 2^-25 half turns (9.4e-8 rad).
+// read.  The phase's top 32 bits are split into a quarter turn and the rest, at
+// most an eighth of a turn, whose sine and cosine are polynomials (turn_sincos):
+// off by 1.1e-7 at most, in about half the instructions of sincospif.
 //
 // The kernel is bound by memory: every number is read and written once.  A
 // thread owns 16 numbers of one token (8 pairs, two 16-byte vectors for 16-bit
@@ -31,12 +32,33 @@ struct RotaryTable {
   float mag;                         // factor on the rotated numbers
 };
 
+// cos and sin of phase / 2^32 turns.  With q the nearest quarter turn and x the
+// rest in half turns, |x| <= 1/4, z = x^2:
+//   sin(pi x) ~ x (s0 + s1 z + s2 z^2 + s3 z^3),  cos(pi x) ~ 1 + z (c0 + c1 z + c2 z^2 + c3 z^3),
+// the Chebyshev interpolants of sin(pi x) / x and (cos(pi x) - 1) / z in z on
+// [0, 1/16]: off by 1.1e-7 at most with fp32's roundings.
+__device__ __forceinline__ void turn_sincos(uint32_t phase, float &c, float &s) {
+  const uint32_t q = (phase + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(phase - (q << 30))) * 4.656612873077393e-10f;   // 2^-31
+  const float z = x * x;
+  float u = fmaf(z, -5.890768766e-01f, 2.549767017e+00f);
+  u = fmaf(u, z, -5.167707920e+00f);
+  u = fmaf(u, z, 3.141592741e+00f) * x;
+  float v = fmaf(z, 2.321258634e-01f, -1.335137844e+00f);
+  v = fmaf(v, z, 4.058710575e+00f);
+  v = fmaf(v, z, -4.934802055e+00f);
+  v = fmaf(v, z, 1.f);
+  // q quarter turns on: (c, s) -> (-s, c) each
+  const float a = q & 1 ? u : v, b = q & 1 ? v : u;
+  c = __uint_as_float(__float_as_uint(a) ^ (((q + 1) & 2) << 30));
+  s = __uint_as_float(__float_as_uint(b) ^ ((q & 2) << 30));
+}
+
 // cos and sin of pair i at the position whose axis numbers are at `pos`
 __device__ __forceinline__ void rotary_angle(const RotaryTable &t, int i, const int32_t *pos, float &c, float &s) {
   const unsigned long long f = t.turns[i];
   const long long p = pos[t.axis[i]];
-  const int32_t phase = static_cast<int32_t>((static_cast<unsigned long long>(p) * f) >> 32);
-  sincospif(static_cast<float>(phase) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+  turn_sincos(static_cast<uint32_t>((static_cast<unsigned long long>(p) * f) >> 32), c, s);
 }
 
 template <typename T>

@@ -19,6 +19,21 @@ from ._lib import McsRotary, check, lib
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _I64x3 = ctypes.c_int64 * 3
+# the current stream's handle without the objects around it (a call takes a few microseconds, they cost two)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(name: str, device, *args) -> None:
+    """The library function on `device`'s current stream, with that device current."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        code = getattr(lib(), name)(*args, _raw_stream(index))
+    else:
+        with api._on(device):
+            code = getattr(lib(), name)(*args, _raw_stream(index))
+    if code:
+        check(code, name)
 
 
 class Rotary:
@@ -64,6 +79,7 @@ class Rotary:
         self.device = self.turns.device
         self._c = McsRotary(self.turns.data_ptr(), self.axis.data_ptr(), dims // 2, int(layout == "interleaved"),
                             len(axes), float(magnitude))
+        self._ref = ctypes.byref(self._c)
 
 
 def _frequencies(m: int, base: float, scaling: Optional[Tuple]):
@@ -97,6 +113,8 @@ def _position_strides(positions: torch.Tensor, B: int, N: int, axes: int, device
     if positions.dtype != torch.int32 or positions.device != device:
         raise ValueError(f"positions must be an int32 tensor on {device}, got {positions.dtype} on {positions.device}")
     shape, stride = tuple(positions.shape), positions.stride()
+    if shape == (B, N, axes) and (axes == 1 or stride[2] == 1):
+        return (0 if B == 1 else stride[0]), stride[1]
     if axes == 1 and shape and shape[-1] != 1 or axes == 1 and len(shape) == 1:
         shape, stride = shape + (1,), stride + (1,)
     elif axes == 1 and len(shape) == 2 and N == 1 and shape[0] == B:      # [B, 1]: one token of each sequence
@@ -120,14 +138,12 @@ def _check_rotary(rotary: "Rotary", d: int, device):
         raise ValueError(f"rotary is on {rotary.device}, the tensor on {device}")
 
 
-def _launch(x: torch.Tensor, positions: torch.Tensor, pos_b: int, pos_n: int, rotary: Rotary, back: bool,
+def _launch(x: torch.Tensor, positions: torch.Tensor, pos_b: int, pos_n: int, rotary: Rotary, back: int,
             out: torch.Tensor) -> None:
     B, H, N, d = x.shape
     sb, sh, sn, _ = x.stride()
-    with api._on(x.device):
-        check(lib().mcs_rotate(x.data_ptr(), _DTYPES[x.dtype], B, H, N, d, _I64x3(sb, sh, sn), positions.data_ptr(),
-                               pos_b, pos_n, ctypes.byref(rotary._c), int(back), out.data_ptr(),
-                               api._stream(x.device)), "mcs_rotate")
+    _run("mcs_rotate", x.device, x.data_ptr(), _DTYPES[x.dtype], B, H, N, d, _I64x3(sb, sh, sn), positions.data_ptr(),
+         pos_b, pos_n, rotary._ref, back, out.data_ptr())
 
 
 def _rows(x: torch.Tensor) -> torch.Tensor:
@@ -135,24 +151,31 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
     return x if x.stride(3) == 1 or x.shape[3] == 1 else x.contiguous()
 
 
+def _empty(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 class _Rotate(torch.autograd.Function):
+    """Turning by the positions, or back; the gradient is the other one."""
+
     @staticmethod
-    def forward(ctx, x, positions, pos_b, pos_n, rotary):
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _launch(x, positions, pos_b, pos_n, rotary, False, out)
+    def forward(ctx, x, positions, pos_b, pos_n, rotary, back):
+        out = _empty(x)
+        _launch(x, positions, pos_b, pos_n, rotary, back, out)
         ctx.save_for_backward(positions)
-        ctx.more = (pos_b, pos_n, rotary)
+        ctx.more = (pos_b, pos_n, rotary, 1 - back)
         return out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         positions, = ctx.saved_tensors
-        pos_b, pos_n, rotary = ctx.more
         grad = _rows(grad)
-        out = torch.empty(grad.shape, dtype=grad.dtype, device=grad.device)
-        _launch(grad, positions, pos_b, pos_n, rotary, True, out)
-        return out, None, None, None, None
+        if torch.is_grad_enabled() and grad.requires_grad:
+            out = _Rotate.apply(grad, positions, *ctx.more)
+        else:
+            out = _empty(grad)
+            _launch(grad, positions, *ctx.more, out)
+        return out, None, None, None, None, None
 
 
 def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -160,7 +183,11 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Option
     pairs turned by the tokens' positions: contiguous [B, H, N, d].
 
     positions: int32 [N] or [B, N], with several axes [N, axes] or
-    [B, N, axes].  Differentiable in x (not with `out`)."""
+    [B, N, axes].  Differentiable in x (not with `out`), any number of times.
+
+    To capture a backward pass into a CUDA graph while an eager graph of the same
+    leaf lives, run the eager one on the capturing stream: torch ties a leaf's
+    gradient to the stream of its first use, and the capture fails otherwise."""
     if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.dtype not in _DTYPES or not x.is_cuda:
         raise ValueError("x must be a CUDA tensor [B, H, N, d] of bf16, fp16 or fp32")
     B, H, N, d = x.shape
@@ -171,10 +198,10 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Option
     if torch.is_grad_enabled() and x.requires_grad:
         if out is not None:
             raise ValueError("rotate with a gradient writes its own output: leave `out` away")
-        return _Rotate.apply(x, positions, pos_b, pos_n, rotary)
+        return _Rotate.apply(x, positions, pos_b, pos_n, rotary, 0)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(x)
     else:
         api._check_tensor(out, "out", x.shape, x.dtype, x.device)
-    _launch(x, positions, pos_b, pos_n, rotary, False, out)
+    _launch(x, positions, pos_b, pos_n, rotary, 0, out)
     return out
