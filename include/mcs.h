@@ -450,8 +450,8 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
 /*
  * mcs_cache_attention -- O = softmax(scale Q K^T) V over the cache's tokens
  * [0, lengths[b]) of each sequence.
- * Q, O: bf16 [B, Hq, Nq, d], contiguous, 16-byte aligned; Hq a multiple of
- *   H: query head h goes by key head h / (Hq / H).  Nq * Hq / H <= 2^20.
+ * Q, O: bf16 [B, Hq, Nq, d], contiguous, 16-byte aligned, no overlap; Hq a
+ *   multiple of H: query head h goes by key head h / (Hq / H).  Nq * Hq / H <= 2^20.
  * lengths: int32 [B]; more than the table holds counts as what it holds and
  *   records MCS_ERR_BAD_META.
  * counts: int32 [B] query tokens of each sequence (rows from counts[b] on give
@@ -459,7 +459,8 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
  * causal: query i of a sequence stands at place lengths[b] - counts[b] + i and
  *   sees the places up to its own; else every query sees all.
  * lse: float32 [B, Hq, Nq] or NULL: log of the sum of exp of a row's scores.
- * A row that sees nothing gives zeros, and -inf in lse.  Weights and products:
+ * A row that sees nothing gives zeros, and -inf in lse; a query that is not
+ * finite gives NaN.  Weights and products:
  * fp32 sums and statistics of exact 8-bit numbers and 16-bit weights.
  * workspace: 16-byte aligned device memory of the size that the first function
  *   gives for the same cache, Hq and Nq (0: none needed), this call's own until

@@ -61,6 +61,8 @@ class KVCache:
     def empty(B: int, H: int, capacity: int, d: int, page: int = 64, device="cuda") -> "KVCache":
         """A cache with room for `capacity` tokens of each of B sequences, the
         pages dealt out in order."""
+        if B < 1 or H < 1 or capacity < 1:
+            raise ValueError(f"B, H and capacity must be positive: got {B}, {H}, {capacity}")
         per = -(-int(capacity) // page)
         n = B * per
         pages = [torch.zeros((n, H, page, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
@@ -162,7 +164,8 @@ def cache_attention(Q: torch.Tensor, cache: KVCache, lengths: torch.Tensor, caus
     causal: query i of a sequence stands at place lengths[b] - counts[b] + i
     and sees the places up to its own.  counts (int32 [B], default Nq): query
     tokens of each sequence; rows behind give zeros, as rows do that see
-    nothing (lse -inf)."""
+    nothing (lse -inf).  A query that is not finite gives NaN.  `out` must not
+    overlap Q.  For inference: no gradient flows through the cache."""
     _check_cache(cache)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 4:
         raise ValueError("Q must be a tensor [B, Hq, Nq, d]")

@@ -74,9 +74,11 @@ class Rotary:
         turns = [round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in self.frequencies]
         turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
         axis = [a for a, m in enumerate(axes) for _ in range(m)]
-        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
-        self.axis = torch.tensor(axis, dtype=torch.int32, device=device)
-        self.device = self.turns.device
+        # one copy to the device: the turns' 64-bit numbers, then the axes' 32-bit ones
+        both = torch.cat([torch.tensor(turns, dtype=torch.int64).view(torch.int32), torch.tensor(axis, dtype=torch.int32)])
+        both = both.to(device)
+        self.turns, self.axis = both[:dims].view(torch.int64), both[dims:]
+        self.device = both.device
         self._c = McsRotary(self.turns.data_ptr(), self.axis.data_ptr(), dims // 2, int(layout == "interleaved"),
                             len(axes), float(magnitude))
         self._ref = ctypes.byref(self._c)

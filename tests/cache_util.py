@@ -48,12 +48,13 @@ def held(cache):
     return k, v
 
 
-def random_cache(B, H, lengths, d, page, seed=0, spread=1.0, spare=3, poison=True):
+def random_cache(B, H, lengths, d, page, seed=0, spread=1.0, spare=3, poison=True, places=0):
     """A cache whose sequences hold `lengths` tokens in pages dealt out of
     order; what no token owns (tails of last pages, spare pages) is NaN, and
-    table entries behind the last page are -1."""
+    table entries behind the last page are -1.  places: the table has room for
+    as many tokens at least (what decides how the work is dealt)."""
     g = torch.Generator().manual_seed(seed)
-    per = max(1, max(-(-n // page) for n in lengths)) + 1
+    per = max(max(1, max(-(-n // page) for n in lengths)) + 1, places // page)
     need = sum(-(-n // page) for n in lengths)
     n_pages = need + spare
     pages, scales = [], []

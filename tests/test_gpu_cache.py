@@ -11,6 +11,10 @@ from tests.cache_util import (F64, assert_attention, attended, held, nearest_e4m
 
 pytestmark = pytest.mark.gpu
 
+# room for more than 64 tiles of 128 tokens: the work is dealt over all SMs, and
+# more than 16 rows of a key head take the tensor-memory kernel
+WIDE = 8320
+
 
 def i32(*v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
@@ -131,10 +135,11 @@ def test_append_rotates_keys(layout, d, dims, axes):
     same_cache(cache, host, rotated_keys=True)
 
 
-def test_numbers_that_are_not_finite():
+@pytest.mark.parametrize("places", [64, WIDE], ids=["clusters", "dealt"])
+def test_numbers_that_are_not_finite(places):
     """+-inf is held as the page's largest number, a token with a NaN as a NaN
     key: rows that see it are NaN, rows that do not are not reached."""
-    cache = mcs.KVCache.empty(1, 1, 64, 64, 32)
+    cache = mcs.KVCache.empty(1, 1, places, 64, 32)
     g = torch.Generator().manual_seed(2)
     K, V = (torch.randn((1, 1, 40, 64), generator=g).to(torch.bfloat16) for _ in range(2))
     K[0, 0, 3, 7], V[0, 0, 5, 1] = math.inf, -math.inf
@@ -152,11 +157,13 @@ def test_numbers_that_are_not_finite():
     assert torch.isfinite(O[0, 0, :30]).all() and O[0, 0, 30:].isnan().all()
     assert mcs.cache_attention(Q, cache, i32(40)).isnan().all()
     assert torch.isfinite(mcs.cache_attention(Q, cache, i32(30))).all()
+    # a query that is not finite gives NaN, and no other row
     Q[0, 0, 4, 0], Q[0, 0, 9, 0] = math.nan, math.inf
-    O = mcs.cache_attention(Q, cache, i32(30))
-    fine = torch.ones(40, dtype=torch.bool)
-    fine[[4, 9]] = False
-    assert torch.isfinite(O[0, 0, fine.cuda()]).all() and O[0, 0, 4].isnan().all()
+    for rows in (40, 10):
+        O = mcs.cache_attention(Q[:, :, :rows].contiguous(), cache, i32(30))
+        fine = torch.ones(rows, dtype=torch.bool)
+        fine[[4, 9]] = False
+        assert torch.isfinite(O[0, 0, fine.cuda()]).all() and O[0, 0, [4, 9]].isnan().all()
 
 
 CASES = [
@@ -188,17 +195,18 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
 @pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
-def test_attention(case):
+def test_attention(case, places):
     B, Hq, H, Nq, d, page, lengths, causal, counts = case
-    cache = random_cache(B, H, lengths, d, page, seed=Nq)
+    cache = random_cache(B, H, lengths, d, page, seed=Nq, places=places)
     g = torch.Generator().manual_seed(9)
     Q = (torch.randn((B, Hq, Nq, d), generator=g) * 1.5).to(torch.bfloat16)
     Q[..., :: 3] *= 0.01
     ref, lse, A, E = attended(Q, cache, lengths, causal, counts)
     O, got_lse = mcs.cache_attention(Q.cuda(), cache, i32(*lengths), causal=causal, return_lse=True,
                                      counts=None if counts is None else i32(*counts))
-    assert_attention(O, ref, A, E, weight=2.0 ** -11 if Nq * Hq // H <= 32 else 2.0 ** -8)
+    assert_attention(O, ref, A, E, weight=2.0 ** -11 if Nq * Hq // H <= 16 else 2.0 ** -8)
     got_lse = got_lse.cpu().to(F64)
     assert torch.equal(got_lse.isinf(), lse.isinf())
     some = ~lse.isinf()
@@ -208,25 +216,27 @@ def test_attention(case):
     assert torch.equal(O, again)
 
 
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
 @pytest.mark.parametrize("Nq", [1, 40, 300])
 @pytest.mark.parametrize("spread", [0.0, 12.0])
-def test_attention_with_far_apart_scales_and_sharp_scores(Nq, spread):
+def test_attention_with_far_apart_scales_and_sharp_scores(Nq, spread, places):
     """Pages whose scales differ by many binades (a row's largest score need not
     carry its largest weight), large and tiny queries, another softmax scale."""
     lengths = [777]
-    cache = random_cache(1, 2, lengths, 64, 16, seed=4, spread=spread)
+    cache = random_cache(1, 2, lengths, 64, 16, seed=4, spread=spread, places=places)
     cache.k_scale.fill_(2.0 ** -7)
     g = torch.Generator().manual_seed(9)
     Q = (torch.randn((1, 2, Nq, 64), generator=g) * torch.exp2(torch.randint(-40, 4, (1, 2, Nq, 1), generator=g).float())).to(torch.bfloat16)
     ref, lse, A, E = attended(Q, cache, lengths, False, scale=0.7)
     O = mcs.cache_attention(Q.cuda(), cache, i32(777), scale=0.7)
     # 2^-25 of the largest weight for those below fp16's normal range: 777 of them at most, on the largest numbers
-    assert_attention(O, ref, A, E, weight=2.0 ** -11 if Nq * 1 <= 32 else 2.0 ** -8)
+    assert_attention(O, ref, A, E, weight=2.0 ** -11 if Nq <= 16 else 2.0 ** -8)
 
 
-def test_bad_pages_and_lengths_are_left_out_and_recorded():
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+def test_bad_pages_and_lengths_are_left_out_and_recorded(places):
     lengths = [200, 64]
-    cache = random_cache(2, 1, lengths, 64, 32, seed=6)
+    cache = random_cache(2, 1, lengths, 64, 32, seed=6, places=places)
     cache.page_table[0, 2] = -7                       # places 64..95 of sequence 0
     cache.page_table[0, 5] = cache.n_pages            # places 160..191
     g = torch.Generator().manual_seed(9)
@@ -320,14 +330,29 @@ def test_graphs_that_share_a_cache_and_streams():
             assert torch.equal(o, e)
 
 
-def test_generation_loop():
+def test_lengths_and_counts_out_of_range():
+    """Negative ones count as none, counts above the call's rows as all of them."""
+    for places in (0, WIDE):
+        cache = random_cache(2, 1, [50, 70], 64, 16, seed=1, places=places, poison=False)
+        g = torch.Generator().manual_seed(3)
+        Q = torch.randn((2, 4, 9, 64), generator=g).to(torch.bfloat16).cuda()
+        O = mcs.cache_attention(Q, cache, i32(-3, 70), counts=i32(9, -1))
+        assert (O == 0).all()
+        assert torch.equal(mcs.cache_attention(Q, cache, i32(50, 70), causal=True, counts=i32(2 ** 31 - 1, 9)),
+                           mcs.cache_attention(Q, cache, i32(50, 70), causal=True))
+        K, V = mcs.cache_read(cache, i32(0, 0), 5, counts=i32(-1, 99))
+        assert (K[0] == 0).all() and (V[0] == 0).all() and (K[1] != 0).any()
+
+
+@pytest.mark.parametrize("capacity", [400, WIDE], ids=["clusters", "dealt"])
+def test_generation_loop(capacity):
     """The operators together, as a generating model uses them: chunks and then
     single tokens, each rotated, appended and attended with everything before;
     against attention in 64 bits over what the cache holds, and the context
     read back for a dense call."""
     B, Hq, H, d, page = 2, 6, 2, 64, 16
     rot = mcs.Rotary(d, scaling=("ntk", 2.0))
-    cache = mcs.KVCache.empty(B, H, 400, d, page)
+    cache = mcs.KVCache.empty(B, H, capacity, d, page)
     host = HostCache(cache)
     g = torch.Generator().manual_seed(11)
     at = [0, 0]

@@ -87,6 +87,16 @@ def test_gradient(layout, dims, axes):
     assert abs(along - (dx.double() * e.double()).sum().item()) <= 2e-6 * (w.double().norm() * e.double().norm()).item()
 
 
+def test_gradient_of_a_gradient():
+    """The gradient is linear in what comes back, so its gradient turns forward again."""
+    rot = mcs.Rotary(64, dims=48)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda") * 1001
+    x, w, e = (torch.randn((1, 2, 9, 64), device="cuda", requires_grad=True) for _ in range(3))
+    dx, = torch.autograd.grad(mcs.rotate(x, pos, rot), x, w, create_graph=True)
+    dw, = torch.autograd.grad(dx, w, e)
+    check(dw, turned(e, pos[None, :, None], rot), torch.float32)
+
+
 def test_gradient_of_a_broadcast_input_and_of_any_layout():
     rot = mcs.Rotary(64)
     pos = torch.arange(5, dtype=torch.int32, device="cuda")
