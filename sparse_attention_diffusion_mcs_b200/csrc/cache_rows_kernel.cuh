@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
       if constexpr (CLUSTER) {
         *reinterpret_cast<float4 *>(oc + r * D + col) = acc;
       } else if (!sg.whole) {
-        *reinterpret_cast<float4 *>(a.m.o + (slot + r) * D + col) = acc;
+        *merge_part(a.m, slot, 16, D, r, col / 4) = acc;
       } else if (row0 + r < sa.n_rows && ok) {
         const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;      // a row that sees nothing is 0
         const int row = row0 + r, i = row / share, hq = sg.h * share + row % share;

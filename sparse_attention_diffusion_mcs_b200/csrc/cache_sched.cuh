@@ -185,7 +185,7 @@ struct MergeItem {
 struct MergeSpace {
   MergeItem *items;              // [n_cta]
   float2 *ml;                    // [2 n_cta, rows]  reference (log2 units) and sum
-  float *o;                      // [2 n_cta, rows, d]
+  float4 *o;                     // [2 n_cta, d / 4, rows]: what neighbouring rows' threads write lies together
 };
 __host__ __device__ inline size_t merge_space(int n_cta, int rows, int d, void *base, MergeSpace *m) {
   const size_t a = (static_cast<size_t>(n_cta) * sizeof(MergeItem) + 15) / 16 * 16;
@@ -194,9 +194,14 @@ __host__ __device__ inline size_t merge_space(int n_cta, int rows, int d, void *
     uint8_t *p = static_cast<uint8_t *>(base);
     m->items = reinterpret_cast<MergeItem *>(p);
     m->ml = reinterpret_cast<float2 *>(p + a);
-    m->o = reinterpret_cast<float *>(p + a + b);
+    m->o = reinterpret_cast<float4 *>(p + a + b);
   }
   return a + b + static_cast<size_t>(n_cta) * 2 * rows * d * sizeof(float);
+}
+
+// numbers 4 quad .. 4 quad + 3 of row r of the slot that `before` rows precede
+__device__ __forceinline__ float4 *merge_part(const MergeSpace &m, size_t before, int rows, int d, int r, int quad) {
+  return m.o + before * (d / 4) + static_cast<size_t>(quad) * rows + r;
 }
 
 struct MergeArgs {
@@ -221,26 +226,32 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
   const int c = blockIdx.x;
   const MergeItem it = a.m.items[c];
   if (it.go_on == 0) return;
-  constexpr int TPR = D / 4, RPC = kMergeThreads / TPR;      // threads per row, rows at once
-  const int col = (threadIdx.x % TPR) * 4;
+  constexpr int RPC = kMergeThreads / (D / 4);               // rows at once
+  // a warp takes 8 rows x 4 quads of numbers: 128-byte lines of the parts, 32 of O
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = warp % (D / 16) * 4 + lane / 8;
   const int row0 = it.block * a.rows;
   const int rows = min(a.rows, a.n_rows - row0);
-  for (int r = blockIdx.y * RPC + threadIdx.x / TPR; r < rows; r += gridDim.y * RPC) {
-    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.rows + r; };
+  for (int r0 = blockIdx.y * RPC; r0 < rows; r0 += gridDim.y * RPC) {
+    const int r = r0 + warp / (D / 16) * 8 + lane % 8;
+    if (r >= rows) continue;
+    auto before = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.rows; };
     // four parts at once, the first four (mostly all) before anything waits for them
     float2 p[4];
     float4 x[4];
     auto load = [&](int k0) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const size_t at = slot(min(k0 + u, it.go_on));
-        p[u] = a.m.ml[at];
-        x[u] = *reinterpret_cast<const float4 *>(a.m.o + at * D + col);
+        p[u] = make_float2(-INFINITY, 0.f);
+        if (k0 + u <= it.go_on) {
+          const size_t at = before(k0 + u);
+          p[u] = a.m.ml[at + r];
+          x[u] = *merge_part(a.m, at, a.rows, D, r, quad);
+        }
       }
     };
     load(0);
     float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
-    for (int k = 4; k <= it.go_on; ++k) mm = fmaxf(mm, a.m.ml[slot(k)].x);
+    for (int k = 4; k <= it.go_on; ++k) mm = fmaxf(mm, a.m.ml[before(k) + r].x);
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 <= it.go_on; k0 += 4) {
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float f = merge_factor(p[u].x, p[u].y, mm);
-        if (k0 + u <= it.go_on && f != 0.f) {                // (NaN counts; a part without keys has no O)
+        if (f != 0.f) {                                      // (NaN counts; a part without keys has no O)
           l = fmaf(p[u].y, f, l);
           acc = make_float4(fmaf(x[u].x, f, acc.x), fmaf(x[u].y, f, acc.y), fmaf(x[u].z, f, acc.z), fmaf(x[u].w, f, acc.w));
         }
@@ -257,9 +268,9 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int row = row0 + r, i = row / a.share, hq = it.h * a.share + row % a.share;
     const size_t at = (static_cast<size_t>(it.b) * a.H * a.share + hq) * a.Nq + i;
-    *reinterpret_cast<uint2 *>(a.O + at * D + col) =
+    *reinterpret_cast<uint2 *>(a.O + at * D + 4 * quad) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && col == 0) a.lse[at] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+    if (a.lse && quad == 0) a.lse[at] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
   }
 }
 

@@ -128,7 +128,8 @@ struct TileCfg {
   static constexpr int OFF_BAR = OFF_SC + NSC * 8 * 16;
   static constexpr int N_BAR = 2 * NK + 2 * NV + 2 * NH + NSC + 10 + 1;
   static constexpr int OFF_XCH = OFF_BAR + 8 * N_BAR;         // 128 x float2: half 1's reference and sum for half 0
-  static constexpr int OFF_MISC = OFF_XCH + BM * 8;
+  static constexpr int OFF_RF = OFF_XCH + BM * 8;             // the rows' factors (scale log2(e) 2^..)
+  static constexpr int OFF_MISC = OFF_RF + ROWS * 4;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int MMA_WARP = 0, LOAD_WARP = 1, CVT_WARP = 4, CVT_THREADS = 128, SOFTMAX_WARP = 8;
   static constexpr int THREADS = 16 * 32;
@@ -473,60 +474,57 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
       };
       const int step = two ? 1 : 2, skip = two ? 0 : half;   // this half's tiles: t0 + skip, + step, ...
       const bool active = n > skip;
+      const size_t first_row = (static_cast<size_t>(sg.b) * sa.H + sg.h) * share * sa.Nq;
       auto address = [&](int x) {                      // row x of the item in Q and O
-        const int i = x / share, hq = sg.h * share + x % share;
-        return (static_cast<size_t>(sg.b) * sa.H * share + hq) * sa.Nq + i;
+        return first_row + (share == 1 ? x : static_cast<size_t>(x % share) * sa.Nq + x / share);
       };
       float m_run = -INFINITY, l_run = 0.f;
       if (active) {
-        // ---- the row's query in two e4m3 parts
-        float rowf;
-        {
-          uint4 w[D / 8];
+        // ---- the queries in two e4m3 parts: a warp takes its 32 rows, D / 8 lanes a row.
+        // (A thread for each row, unrolled over the row, took 7 us a part: its
+        // instructions came from far away, its loads 16 bytes a line.)
+        constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes per row, rows at once
+        const int lane_row = (warp & 3) * 32 + lane / LPR, qc = lane % LPR;
+        uint8_t *qs = smem + C::OFF_Q + half * 2 * C::Q_BYTES;
+        float *rf = reinterpret_cast<float *>(smem + C::OFF_RF) + half * C::BM;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 8 * RPI) {
+          uint4 w[8];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
-          if (row < sa.n_rows) {
-            const uint4 *q = reinterpret_cast<const uint4 *>(a.Q + address(row) * D);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) w[c] = __ldg(q + c);
+          for (int i = 0; i < 8; ++i) {
+            const int x = row0 + lane_row + i0 + i * RPI;
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (x < sa.n_rows) w[i] = __ldg(reinterpret_cast<const uint4 *>(a.Q + address(x) * D) + qc);
           }
-          uint32_t am = 0;                             // the largest magnitude, as bf16 bits
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          for (int i = 0; i < 8; ++i) {
+            const int qr = lane_row + i0 + i * RPI;
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t am = 0;                           // the row's largest magnitude, as bf16 bits
 #pragma unroll
-            for (int i = 0; i < 4; ++i) am = max(am, max((x[i] << 1) & 0xFFFEu, (x[i] >> 15) & 0xFFFEu));
-          }
-          const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-          rowf = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-          if (am >> 8 == 255) rowf = __uint_as_float(0x7FC00000u);   // a query that is not finite: NaN
-          uint8_t *qs = smem + C::OFF_Q + half * 2 * C::Q_BYTES;
+            for (int k = 0; k < 4; ++k) am = max(am, max((x[k] << 1) & 0xFFFEu, (x[k] >> 15) & 0xFFFEu));
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const uint32_t x[8] = {w[2 * c].x,     w[2 * c].y,     w[2 * c].z,     w[2 * c].w,
-                                   w[2 * c + 1].x, w[2 * c + 1].y, w[2 * c + 1].z, w[2 * c + 1].w};
+            for (int o = LPR / 2; o; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+            const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+            const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+            if (qc == 0) rf[qr] = am >> 8 == 255 ? __uint_as_float(0x7FC00000u) : down;   // a query that is not finite: NaN
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t hh[2], ll[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float f0 = __uint_as_float(x[2 * i + k] << 16) * up;
-                const float f1 = __uint_as_float(x[2 * i + k] & 0xFFFF0000u) * up;
-                hh[k] = e4m3x2(f0, f1);
-                const float2 back = float2_of_half2(half2_of_e4m3x2(hh[k]));
-                ll[k] = e4m3x2(f0 - back.x, f1 - back.y);
-              }
-              hi[i] = hh[0] | hh[1] << 16;
-              lo[i] = ll[0] | ll[1] << 16;
+            for (int k = 0; k < 4; ++k) {
+              const float f0 = __uint_as_float(x[k] << 16) * up, f1 = __uint_as_float(x[k] & 0xFFFF0000u) * up;
+              hi[k] = e4m3x2(f0, f1);
+              const float2 back = float2_of_half2(half2_of_e4m3x2(hi[k]));
+              lo[k] = e4m3x2(f0 - back.x, f1 - back.y);
             }
-            *reinterpret_cast<uint4 *>(qs + swizzled<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(qs + C::Q_BYTES + swizzled<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            uint8_t *to = qs + swizzled<D>(qr, qc >> 1) + (qc & 1) * 8;
+            *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2 *>(to + C::Q_BYTES) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           }
-          fence_proxy_async_smem();
-          warp_arrive(b_q(half));
         }
+        fence_proxy_async_smem();
+        warp_arrive(b_q(half));
+        const float rowf = rf[r];
         const int lim = limit_of(row);
         const int all = min(limit_of(row0), limit_of(min(row0 + C::BM, sa.n_rows) - 1));   // keys every row sees
         it += skip;
@@ -685,16 +683,17 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
         if (a.lse && orow < sa.n_rows)
           a.lse[at] = l_run == 0.f ? -INFINITY : (ref + log2f(l_run)) * 0.6931471805599453f;
       } else {
-        const size_t slot = (2 * static_cast<size_t>(cta) + (sg.first ? 1 : 0)) * C::ROWS + half * C::BM + r;
-        a.m.ml[slot] = make_float2(ref, l_run);
+        const size_t slot_rows = (2 * static_cast<size_t>(cta) + (sg.first ? 1 : 0)) * C::ROWS;   // rows before the slot's
+        a.m.ml[slot_rows + half * C::BM + r] = make_float2(ref, l_run);
         if (has) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             float o[32];
             load_o(cc, o);
-            float4 *op = reinterpret_cast<float4 *>(a.m.o + slot * D + cc * 32);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) op[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            for (int u = 0; u < 8; ++u)
+              *merge_part(a.m, slot_rows, C::ROWS, D, half * C::BM + r, cc * 8 + u) =
+                  make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
           }
         }
         if (tid == C::SOFTMAX_WARP * 32 && sg.first) {
