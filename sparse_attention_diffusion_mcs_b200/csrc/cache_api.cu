@@ -194,8 +194,14 @@ cudaError_t launch_merge(const CacheAttnArgs &a, const AttnPlan &p, cudaStream_t
   m.share = a.s.share;
   m.n_rows = a.s.n_rows;
   m.rows = p.block;
+  // four parts an item, or more: split them
+  const long long items = static_cast<long long>(a.s.B) * a.s.H * a.s.n_blocks;
+  const int rows = a.s.n_rows < p.block ? a.s.n_rows : p.block;
   const int at_once = kMergeThreads / (D / 4);
-  cache_merge_kernel<D><<<dim3(p.ctas, (p.block + at_once - 1) / at_once), kMergeThreads, 0, s>>>(m);
+  if (4 * items <= p.ctas)
+    cache_merge_kernel<D, true><<<dim3(p.ctas, (rows + 7) / 8 * (D / 16)), kMergeThreads, 0, s>>>(m);
+  else
+    cache_merge_kernel<D, false><<<dim3(p.ctas, (rows + at_once - 1) / at_once), kMergeThreads, 0, s>>>(m);
   return cudaGetLastError();
 }
 

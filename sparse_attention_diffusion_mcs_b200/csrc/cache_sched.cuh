@@ -218,59 +218,97 @@ __device__ __forceinline__ float merge_factor(float m, float l, float mm) {
   return l != l ? l : m == -INFINITY ? 0.f : ex2_approx(m - mm);
 }
 
-// CTA (c, y): rows y, y + gridDim.y, ... (in steps of the rows that a CTA
-// takes at once) of the item that begins in CTA c.  Bound by reading the parts
-// once, out of the second-level cache.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const __grid_constant__ MergeArgs a) {
+// the parts of one row's quad of numbers, added up
+struct MergeSum {
+  float m, l;                    // joint reference and sum
+  float4 acc;
+};
+__device__ __forceinline__ void merge_add(MergeSum &s, float m, float l, const float4 &x, float mm) {
+  const float f = merge_factor(m, l, mm);
+  if (f != 0.f) {                                          // (NaN counts; a part without keys has no O)
+    s.l = fmaf(l, f, s.l);
+    s.acc = make_float4(fmaf(x.x, f, s.acc.x), fmaf(x.y, f, s.acc.y), fmaf(x.z, f, s.acc.z), fmaf(x.w, f, s.acc.w));
+  }
+}
+__device__ __forceinline__ MergeSum merge_parts(const MergeArgs &a, int c, int go_on, int d, int r, int quad, int k0,
+                                                int step) {
+  auto before = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.rows; };
+  // two parts at once, the first two (mostly all) before anything waits for them
+  float2 p[2];
+  float4 x[2];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      p[u] = make_float2(-INFINITY, 0.f);
+      if (k + u * step <= go_on) {
+        const size_t at = before(k + u * step);
+        p[u] = a.m.ml[at + r];
+        x[u] = *merge_part(a.m, at, a.rows, d, r, quad);
+      }
+    }
+  };
+  load(k0);
+  MergeSum s;
+  s.m = fmaxf(p[0].x, p[1].x);
+#pragma unroll 4
+  for (int k = k0 + 2 * step; k <= go_on; k += step) s.m = fmaxf(s.m, a.m.ml[before(k) + r].x);
+  s.l = 0.f;
+  s.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = k0; k <= go_on; k += 2 * step) {
+    if (k > k0) load(k);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) merge_add(s, p[u].x, p[u].y, x[u], s.m);
+  }
+  return s;
+}
+
+// CTA (c, y): a share of the item that begins in CTA c.  A warp takes 8 rows x 4
+// quads of numbers: 128-byte lines of the parts, 32 bytes of O.  Few parts an
+// item: the warps take rows y, y + gridDim.y, ... (in steps of what a CTA takes
+// at once).  Many (SPLIT): all eight warps take the same 8 rows and 4 quads, of
+// every eighth part each, and add up through shared memory, in the warps' order.
+// Either way bound by a few reads that wait for one another: the item, then
+// the parts, out of the second-level cache.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kMergeThreads, 6) cache_merge_kernel(const __grid_constant__ MergeArgs a) {
   const int c = blockIdx.x;
   const MergeItem it = a.m.items[c];
   if (it.go_on == 0) return;
-  constexpr int RPC = kMergeThreads / (D / 4);               // rows at once
-  // a warp takes 8 rows x 4 quads of numbers: 128-byte lines of the parts, 32 of O
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = warp % (D / 16) * 4 + lane / 8;
+  constexpr int QG = D / 16;                                 // groups of 4 quads
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = it.block * a.rows;
   const int rows = min(a.rows, a.n_rows - row0);
-  for (int r0 = blockIdx.y * RPC; r0 < rows; r0 += gridDim.y * RPC) {
-    const int r = r0 + warp / (D / 16) * 8 + lane % 8;
-    if (r >= rows) continue;
-    auto before = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.rows; };
-    // four parts at once, the first four (mostly all) before anything waits for them
-    float2 p[4];
-    float4 x[4];
-    auto load = [&](int k0) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        p[u] = make_float2(-INFINITY, 0.f);
-        if (k0 + u <= it.go_on) {
-          const size_t at = before(k0 + u);
-          p[u] = a.m.ml[at + r];
-          x[u] = *merge_part(a.m, at, a.rows, D, r, quad);
-        }
-      }
-    };
-    load(0);
-    float mm = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
-    for (int k = 4; k <= it.go_on; ++k) mm = fmaxf(mm, a.m.ml[before(k) + r].x);
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 <= it.go_on; k0 += 4) {
-      if (k0) load(k0);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float f = merge_factor(p[u].x, p[u].y, mm);
-        if (f != 0.f) {                                      // (NaN counts; a part without keys has no O)
-          l = fmaf(p[u].y, f, l);
-          acc = make_float4(fmaf(x[u].x, f, acc.x), fmaf(x[u].y, f, acc.y), fmaf(x[u].z, f, acc.z), fmaf(x[u].w, f, acc.w));
-        }
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  auto finish = [&](const MergeSum &s, int r, int quad) {
+    const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
     const int row = row0 + r, i = row / a.share, hq = it.h * a.share + row % a.share;
     const size_t at = (static_cast<size_t>(it.b) * a.H * a.share + hq) * a.Nq + i;
     *reinterpret_cast<uint2 *>(a.O + at * D + 4 * quad) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && quad == 0) a.lse[at] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+        make_uint2(pack_bf16x2(s.acc.x * inv, s.acc.y * inv), pack_bf16x2(s.acc.z * inv, s.acc.w * inv));
+    if (a.lse && quad == 0) a.lse[at] = s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * 0.6931471805599453f;
+  };
+  if constexpr (SPLIT) {
+    __shared__ MergeSum part[8][32];
+    const int r = blockIdx.y / QG * 8 + lane % 8, quad = blockIdx.y % QG * 4 + lane / 8;
+    if (r < rows) part[warp][lane] = merge_parts(a, c, it.go_on, D, r, quad, warp, 8);
+    __syncthreads();
+    if (warp == 0 && r < rows) {
+      MergeSum s;
+      s.m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s.m = fmaxf(s.m, part[w][lane].m);
+      s.l = 0.f;
+      s.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) merge_add(s, part[w][lane].m, part[w][lane].l, part[w][lane].acc, s.m);
+      finish(s, r, quad);
+    }
+  } else {
+    constexpr int RPC = kMergeThreads / (D / 4);             // rows at once
+    const int quad = warp % QG * 4 + lane / 8;
+    for (int r0 = blockIdx.y * RPC; r0 < rows; r0 += gridDim.y * RPC) {
+      const int r = r0 + warp / QG * 8 + lane % 8;
+      if (r < rows) finish(merge_parts(a, c, it.go_on, D, r, quad, 0, 1), r, quad);
+    }
   }
 }
 
