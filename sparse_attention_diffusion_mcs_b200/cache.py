@@ -26,7 +26,10 @@ _I64x3 = ctypes.c_int64 * 3
 class KVCache:
     """The cache's buffers: k_pages, v_pages float8_e4m3fn [n_pages, H, page, d],
     k_scale, v_scale float32 [n_pages, H], page_table int32 [B, max_pages].
-    Token j of sequence b is slot j % page of page page_table[b, j // page]."""
+    Token j of sequence b is slot j % page of page page_table[b, j // page].
+
+    Calls work on these very buffers: change their contents in place (new pages
+    in page_table, for instance); for other buffers make another KVCache."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                  page_table: torch.Tensor):
@@ -51,6 +54,12 @@ class KVCache:
         self._c = McsCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                            page_table.data_ptr(), n_pages, max_pages, B, H, page, d)
         self._ref = ctypes.byref(self._c)
+
+    def __setattr__(self, name, value):
+        # the library holds the buffers' addresses: another tensor under the name would not be seen
+        if name in self.__dict__:
+            raise AttributeError(f"{name} belongs to the cache: change it in place, or make another KVCache")
+        super().__setattr__(name, value)
 
     @property
     def capacity(self) -> int:

@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
   }
   if (tid == C::SOFTMAX_WARP * 32) a.m.items[cta].go_on = 0;   // (the thread that may set it)
   if (warp == C::MMA_WARP) {
+    __syncwarp();                                  // (lane 0 comes from the branch above)
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }

@@ -137,6 +137,11 @@ def test_buffers_of_a_cache():
         b[i] = bad
         with pytest.raises((ValueError, TypeError)):
             mcs.KVCache(*b)
+    with pytest.raises(AttributeError):
+        c.page_table = good[4].clone()                               # the calls would not see it
+    for bad in ((0, 2, 64), (2, 0, 64), (2, 2, 0)):
+        with pytest.raises(ValueError):
+            mcs.KVCache.empty(*bad, 64, device="cpu")
     with pytest.raises(ValueError):
         mcs.cache_read(c, torch.zeros(2, dtype=torch.int32), 3)      # not on a CUDA device
     with pytest.raises(TypeError):

@@ -262,7 +262,6 @@ def test_bad_pages_and_lengths_are_left_out_and_recorded(places):
     assert torch.equal(before[0], cache.k_pages.view(torch.uint8)) and torch.equal(before[1], cache.v_pages.view(torch.uint8))
     # lengths beyond the table's places count as those
     full = random_cache(1, 1, [96], 64, 32, seed=8)
-    full.page_table = None
     short = mcs.KVCache(full.k_pages, full.v_pages, full.k_scale, full.v_scale,
                         torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"))
     short.k_pages.view(torch.uint8).bitwise_and_(0xBF)
