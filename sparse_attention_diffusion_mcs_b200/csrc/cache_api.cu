@@ -25,17 +25,16 @@ cudaStream_t cu(mcs_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 constexpr int kSms = 148;   // of a B200: the grids are sized for it, no result depends on it
 
-// a kernel's dynamic shared memory limit (and clusters of more than 8 CTAs), set once per device
+// a kernel's dynamic shared memory limit, set once per device
 template <auto *Kernel>
-cudaError_t allow_smem(int bytes, bool clusters = false) {
+cudaError_t allow_smem(int bytes) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
   const cudaError_t ge = cudaGetDevice(&dev);
   if (ge != cudaSuccess) return ge;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -111,10 +110,11 @@ struct AttnPlan {
   int split;                     // CTAs of a cluster
 };
 // By sizes known here (the table's places; lengths are not):
-// - Little work: clusters of 16 CTAs at most, as many as fill the SMs once and
-//   as there can be tiles, on blocks of 16 rows.  More rows than 16 read the
-//   keys once a block, but start at once: 20 rows of 16 heads against 8191
-//   tokens took 26 us as one block of 32, 25 with the tile kernel and 5 of merge.
+// - Little work: clusters of 8 CTAs at most (of 16, fewer fit at once: one token
+//   of 16 heads against 8000 20.7 us, of 8 16.0), as many as run at once and as
+//   there can be tiles, on blocks of 16 rows.  More rows than 16 read the keys
+//   once a block, but start at once: 20 rows of 16 heads against 8191 tokens take
+//   15.5 us, as one block of 32 rows 26, with the tile kernel 25 and 5 of merge.
 // - Else 16 rows or fewer are bound by reading the keys (cache_rows_kernel: 16 rows
 //   of 64 heads, 819200 tokens, 294 us; the tile kernel 467), more by the products
 //   (32 rows: the tile kernel 467, blocks of 32 rows 1276).
@@ -126,9 +126,12 @@ AttnPlan plan_attention(const CacheView &c, int B, long long n_rows) {
   p.block = 16;
   p.ctas = 2 * kSms;
   p.split = 1;
-  if (tiles <= 64 && items * tiles <= 16ll * kSms) {
-    long long split = p.ctas / items;
-    split = split > 16 ? 16 : split;
+  if (tiles <= 64 && items * tiles <= 28ll * kSms) {
+    // a cluster lies within one of 8 groups of 16 SMs or more: those that hold
+    // whole clusters, two CTAs an SM, run all of them at once
+    const long long per_group = (items + 7) / 8;
+    long long split = 2 * 16 / per_group;
+    split = split > kMaxRanks ? kMaxRanks : split;
     split = split > tiles ? tiles : split;
     p.split = static_cast<int>(split < 1 ? 1 : split);
     p.ctas = 0;
@@ -150,7 +153,7 @@ cudaError_t launch_rows(CacheAttnArgs &a, const AttnPlan &p, cudaStream_t s) {
     cache_rows_kernel<D, false><<<p.ctas, C::THREADS, C::SMEM, s>>>(a);
     return cudaGetLastError();
   }
-  const cudaError_t e = allow_smem<cache_rows_kernel<D, true>>(C::SMEM, true);
+  const cudaError_t e = allow_smem<cache_rows_kernel<D, true>>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.split), static_cast<unsigned>(a.s.B * a.s.H),

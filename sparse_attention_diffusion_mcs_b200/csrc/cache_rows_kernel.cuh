@@ -98,11 +98,11 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ float ld_dsmem(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float2 ld_dsmem2(uint32_t addr, uint32_t rank) {
   uint32_t r;
-  float v;
+  float2 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(r) : "memory");
   return v;
 }
 __device__ __forceinline__ float4 ld_dsmem4(uint32_t addr, uint32_t rank) {
@@ -129,8 +129,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// weights are held times 2^kBias in fp16
+// weights are held times 2^kRowsBias in fp16
 constexpr float kRowsBias = 14.f;
+constexpr int kMaxRanks = 8;     // CTAs of a cluster, at most
 
 template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
@@ -560,16 +561,25 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
       const int rows_here = min(16, sa.n_rows - row0);
       for (int idx = rank * C::THREADS + tid; idx < rows_here * (D / 4); idx += ranks * C::THREADS) {
         const int r = idx / (D / 4), c = (idx - r * (D / 4)) * 4;
+        // all ranks' reads on the way at once: one after the other they took 3 to 5 us
+        float2 p[kMaxRanks];
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) p[k] = ld_dsmem2(sbase + C::OFF_ML + r * 8, min(k, ranks - 1));
+        float4 x[kMaxRanks];
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) x[k] = ld_dsmem4(sbase + C::OFF_O + (r * D + c) * 4, min(k, ranks - 1));
         float mm = -INFINITY;
-        for (int k = 0; k < ranks; ++k) mm = fmaxf(mm, ld_dsmem(sbase + C::OFF_ML + r * 8, k));
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) mm = fmaxf(mm, p[k].x);
         float ll = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < ranks; ++k) {
-          const float pm = ld_dsmem(sbase + C::OFF_ML + r * 8, k), pl = ld_dsmem(sbase + C::OFF_ML + r * 8 + 4, k);
-          const float f = merge_factor(pm, pl, mm);
-          const float4 x = ld_dsmem4(sbase + C::OFF_O + (r * D + c) * 4, k);
-          ll = fmaf(pl, f, ll);
-          acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) {
+          const float f = k < ranks ? merge_factor(p[k].x, p[k].y, mm) : 0.f;
+          if (f != 0.f) {                                // (NaN counts)
+            ll = fmaf(p[k].y, f, ll);
+            acc = make_float4(fmaf(x[k].x, f, acc.x), fmaf(x[k].y, f, acc.y), fmaf(x[k].z, f, acc.z), fmaf(x[k].w, f, acc.w));
+          }
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;      // a row that sees nothing is 0
         const int row = row0 + r, i = row / share, hq = run.h * share + row % share;
