@@ -68,11 +68,6 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float y = fabsf(x);
-  return y < __uint_as_float(0x7F800000u) ? y : 0.f;   // inf and NaN count as 0
-}
-
 struct AppendArgs {
   CacheView c;
   const bf16 *K, *V;
@@ -121,7 +116,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_
 
   float kx[U][8], ky[U][8];
   RotVec<bf16> v0[U], v1[U];
-  float ak = 0.f, av = 0.f;
+  uint32_t ak = 0, av = 0;                                    // largest finite magnitudes, as their bits
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int id = tid + j * threads, slot = lo + (id >> shift), u = id & (upt - 1);
@@ -143,17 +138,35 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_
         rotary_unit_angles(a.t, r, a.pos ? a.pos + b * a.pos_b + i * a.pos_n : &place, cs, sn);
         rotary_turn(a.t.interleaved, cs, sn, kx[j], ky[j]);
       }
-      float x[8], y[8];
-      v0[j].get(x);
-      v1[j].get(y);
-      bool bad = false;
+      // magnitudes by their bits, which order as they do; only a unit with a number
+      // that is not finite looks at each
+      constexpr uint32_t kAbs = 0x7FFFFFFFu, kInf = 0x7F800000u;
+      const uint32_t w[8] = {v0[j].u.x, v0[j].u.y, v0[j].u.z, v0[j].u.w, v1[j].u.x, v1[j].u.y, v1[j].u.z, v1[j].u.w};
+      uint32_t mk = 0, mv = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        ak = fmaxf(ak, fmaxf(finite_abs(kx[j][e]), finite_abs(ky[j][e])));
-        av = fmaxf(av, fmaxf(finite_abs(x[e]), finite_abs(y[e])));
-        bad |= isnan(kx[j][e]) || isnan(ky[j][e]) || isnan(x[e]) || isnan(y[e]);
+        mk = max(mk, max(__float_as_uint(kx[j][e]) & kAbs, __float_as_uint(ky[j][e]) & kAbs));
+        mv = max(mv, max(w[e] << 16 & kAbs, w[e] & 0x7FFF0000u));
       }
-      if (bad) s_nan[slot] = 1;
+      if (max(mk, mv) >= kInf) {
+        mk = mv = 0;
+        bool bad = false;
+        auto look = [&](uint32_t x, uint32_t &m) {
+          x &= kAbs;
+          if (x < kInf) m = max(m, x);
+          bad |= x > kInf;
+        };
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          look(__float_as_uint(kx[j][e]), mk);
+          look(__float_as_uint(ky[j][e]), mk);
+          look(w[e] << 16, mv);
+          look(w[e] & 0xFFFF0000u, mv);
+        }
+        if (bad) s_nan[slot] = 1;
+      }
+      ak = max(ak, mk);
+      av = max(av, mv);
     }
   }
   if (pid < 0 || pid >= c.n_pages) {   // behind the table, or no page of the pool: nothing is written
@@ -167,9 +180,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_
     ok = c.k_scale[sidx];
     ov = c.v_scale[sidx];
   }
-  // magnitudes order as their bits do
-  const unsigned mk = __reduce_max_sync(0xffffffffu, __float_as_uint(ak));
-  const unsigned mv = __reduce_max_sync(0xffffffffu, __float_as_uint(av));
+  const unsigned mk = __reduce_max_sync(0xffffffffu, ak);
+  const unsigned mv = __reduce_max_sync(0xffffffffu, av);
   if ((tid & 31) == 0) {
     atomicMax(&s_amax[0], mk);
     atomicMax(&s_amax[1], mv);
@@ -202,29 +214,29 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_
     if (slot < hi) {
       const RotUnit r = rotary_unit(a.t, u);
       const bool bad = s_nan[slot] != 0;
-      auto pack = [&](const float (&x)[8], float f, bool value) {
+      auto pack = [&](const float (&x)[8], float f) {
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p = x[2 * e] * f, q = x[2 * e + 1] * f;
-          if (value) {   // a value's NaN is held as 0
-            p = isnan(p) ? 0.f : p;
-            q = isnan(q) ? 0.f : q;
-          }
-          w[e] = e4m3x2(p, q);
-        }
-        uint2 o = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        if (bad && !value) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        return o;
+        for (int e = 0; e < 4; ++e) w[e] = e4m3x2(x[2 * e] * f, x[2 * e + 1] * f);
+        return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
       };
-      uint8_t *kp = c.k + (row0 + slot) * c.d, *vp = c.v + (row0 + slot) * c.d;
-      *reinterpret_cast<uint2 *>(kp + r.first) = pack(kx[j], ik, false);
-      *reinterpret_cast<uint2 *>(kp + r.second) = pack(ky[j], ik, false);
       float x[8], y[8];
       v0[j].get(x);
       v1[j].get(y);
-      *reinterpret_cast<uint2 *>(vp + r.first) = pack(x, iv, true);
-      *reinterpret_cast<uint2 *>(vp + r.second) = pack(y, iv, true);
+      uint2 k0 = pack(kx[j], ik), k1 = pack(ky[j], ik);
+      if (bad) {                                              // a NaN key, its values' NaN as 0
+        k0 = k1 = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = isnan(x[e]) ? 0.f : x[e];
+          y[e] = isnan(y[e]) ? 0.f : y[e];
+        }
+      }
+      uint8_t *kp = c.k + (row0 + slot) * c.d, *vp = c.v + (row0 + slot) * c.d;
+      *reinterpret_cast<uint2 *>(kp + r.first) = k0;
+      *reinterpret_cast<uint2 *>(kp + r.second) = k1;
+      *reinterpret_cast<uint2 *>(vp + r.first) = pack(x, iv);
+      *reinterpret_cast<uint2 *>(vp + r.second) = pack(y, iv);
     }
   }
   if (tid == 0) {
