@@ -5,7 +5,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <type_traits>
 
 #include "../../include/mcs.h"
 #include "cache_rows_kernel.cuh"

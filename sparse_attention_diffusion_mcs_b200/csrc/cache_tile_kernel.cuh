@@ -44,6 +44,8 @@
 // pipe (one in eight 1.81, one in four 1.98).
 #pragma once
 
+#include <type_traits>
+
 #include "cache_rows_kernel.cuh"
 
 namespace mcs {
