@@ -93,10 +93,12 @@ cudaError_t launch_rotate(RotateArgs &a, bool vec, cudaStream_t s) {
   groups = groups < 1 ? 1 : (groups > a.H ? a.H : groups);
   a.heads = static_cast<int>((a.H + groups - 1) / groups);
   const dim3 grid(static_cast<unsigned>(blocks), (a.H + a.heads - 1) / a.heads);
-  if (vec)
-    rotate_kernel<T, true><<<grid, kRotateThreads, 0, s>>>(a);
+  if (!vec)
+    rotate_kernel<T, false, false><<<grid, kRotateThreads, 0, s>>>(a);
+  else if (a.t.pairs % 8 == 0)
+    rotate_kernel<T, true, false><<<grid, kRotateThreads, 0, s>>>(a);
   else
-    rotate_kernel<T, false><<<grid, kRotateThreads, 0, s>>>(a);
+    rotate_kernel<T, true, true><<<grid, kRotateThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(const __grid_
         const int32_t place = base + slot;
         float cs[8], sn[8];
         rotary_unit_angles(a.t, r, a.pos ? a.pos + b * a.pos_b + i * a.pos_n : &place, cs, sn);
-        rotary_turn(a.t.interleaved, cs, sn, kx[j], ky[j]);
+        rotary_turn(a.t.interleaved, r.n_rot, cs, sn, kx[j], ky[j]);
       }
       // magnitudes by their bits, which order as they do; only a unit with a number
       // that is not finite looks at each

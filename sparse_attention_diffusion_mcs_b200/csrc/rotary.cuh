@@ -63,8 +63,15 @@ __device__ __forceinline__ void rotary_angle(const RotaryTable &t, int i, const 
   turn_sincos(static_cast<uint32_t>((static_cast<unsigned long long>(p) * f) >> 32), c, s);
 }
 
+// 8 numbers; keep(was, n): the neighbouring pairs from the n-th on as in `was`, bit for bit
 template <typename T>
-struct RotVec;   // 8 numbers
+struct RotVec;
+__device__ __forceinline__ void keep_words(uint4 &u, const uint4 &was, int n) {
+  if (n <= 0) u.x = was.x;
+  if (n <= 1) u.y = was.y;
+  if (n <= 2) u.z = was.z;
+  if (n <= 3) u.w = was.w;
+}
 template <>
 struct RotVec<float> {
   float4 a, b;
@@ -82,6 +89,12 @@ struct RotVec<float> {
   __device__ __forceinline__ void set(const float (&v)[8]) {
     a = make_float4(v[0], v[1], v[2], v[3]);
     b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void keep(const RotVec &was, int n) {
+    if (n <= 0) a.x = was.a.x, a.y = was.a.y;
+    if (n <= 1) a.z = was.a.z, a.w = was.a.w;
+    if (n <= 2) b.x = was.b.x, b.y = was.b.y;
+    if (n <= 3) b.z = was.b.z, b.w = was.b.w;
   }
 };
 template <>
@@ -101,6 +114,7 @@ struct RotVec<bf16> {
     u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                    pack_bf16x2(v[6], v[7]));
   }
+  __device__ __forceinline__ void keep(const RotVec &was, int n) { keep_words(u, was.u, n); }
 };
 template <>
 struct RotVec<__half> {
@@ -125,6 +139,7 @@ struct RotVec<__half> {
     }
     u = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  __device__ __forceinline__ void keep(const RotVec &was, int n) { keep_words(u, was.u, n); }
 };
 
 __device__ __forceinline__ float rot_get(float x) { return x; }
@@ -163,7 +178,7 @@ __device__ __forceinline__ RotUnit rotary_unit(const RotaryTable &t, int u) {
   return r;
 }
 
-// cos and sin (times mag) of the unit's pairs; (1, 0) for pairs that stay
+// cos and sin (times mag) of the unit's pairs that turn
 __device__ __forceinline__ void rotary_unit_angles(const RotaryTable &t, const RotUnit &r, const int32_t *pos,
                                                    float (&c)[8], float (&s)[8]) {
 #pragma unroll
@@ -178,18 +193,17 @@ __device__ __forceinline__ void rotary_unit_angles(const RotaryTable &t, const R
   }
 }
 
-// the unit's 16 numbers turned in place: x its first vector, y its second
-__device__ __forceinline__ void rotary_turn(bool interleaved, const float (&c)[8], const float (&s)[8], float (&x)[8],
-                                            float (&y)[8]) {
+// the unit's first n_rot pairs turned in place, the others untouched (b * 0 is not 0
+// where b is inf or NaN): x its first vector, y its second.  Half layout: n_rot is 8.
+__device__ __forceinline__ void rotary_turn(bool interleaved, int n_rot, const float (&c)[8], const float (&s)[8],
+                                            float (&x)[8], float (&y)[8]) {
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = fmaf(a, c[i], -b * s[i]);
-      x[2 * i + 1] = fmaf(a, s[i], b * c[i]);
-      const float e = y[2 * i], f = y[2 * i + 1];
-      y[2 * i] = fmaf(e, c[4 + i], -f * s[4 + i]);
-      y[2 * i + 1] = fmaf(e, s[4 + i], f * c[4 + i]);
+    for (int i = 0; i < 8; ++i) {
+      float &p = i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)], &q = i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1];
+      const float a = p, b = q;
+      p = i < n_rot ? fmaf(a, c[i], -b * s[i]) : a;
+      q = i < n_rot ? fmaf(a, s[i], b * c[i]) : b;
     }
   } else {
 #pragma unroll
@@ -216,9 +230,12 @@ struct RotateArgs {
 constexpr int kRotateThreads = 256;
 
 // VEC: 16-byte vectors (see the host's rule); else one pair per thread, for
-// any strides, alignment and number of pairs.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+// any strides, alignment and number of pairs.  Numbers that stay keep their bits.
+// MIXED: some unit has pairs of both kinds (interleaved, pairs no multiple of 8); a
+// kernel of its own, whose kept vectors would cost the other a CTA of three on an SM.
+template <typename T, bool VEC, bool MIXED>
+__global__ void __launch_bounds__(kRotateThreads, VEC && !MIXED ? 3 : 1)
+    rotate_kernel(const __grid_constant__ RotateArgs a) {
   const int per_token = VEC ? a.d / 16 : a.d - a.t.pairs;   // units, or pairs and single numbers behind them
   const long long id = static_cast<long long>(blockIdx.x) * kRotateThreads + threadIdx.x;
   const long long token = id / per_token;
@@ -239,12 +256,18 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const __grid_con
       for (int i = 0; i < 8; ++i) s[i] = -s[i];
     }
     auto turn = [&](RotVec<T> &vx, RotVec<T> &vy) {
+      if (r.n_rot == 0) return;
+      const RotVec<T> was_x = vx, was_y = vy;
       float x[8], y[8];
       vx.get(x);
       vy.get(y);
-      rotary_turn(a.t.interleaved || r.n_rot == 0, c, s, x, y);
+      rotary_turn(a.t.interleaved, 8, c, s, x, y);
       vx.set(x);
       vy.set(y);
+      if (MIXED) {
+        vx.keep(was_x, r.n_rot);
+        vy.keep(was_y, r.n_rot - 4);
+      }
     };
     constexpr int U = sizeof(T) == 4 ? 2 : 4;   // heads in flight
     int h = h0;
