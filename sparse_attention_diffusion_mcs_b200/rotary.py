@@ -13,6 +13,7 @@ import math
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import api
 from ._lib import McsRotary, check, lib
@@ -157,27 +158,46 @@ def _empty(x: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
+def _differentiated(x: torch.Tensor) -> bool:
+    """Whether a gradient or a tangent (forward mode) goes through x."""
+    if torch.is_grad_enabled() and x.requires_grad:
+        return True
+    # (no level is open: no tangents; unpack_dual alone would take 0.4 us to say so)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(x).tangent is not None
+
+
+def _turned(x: torch.Tensor, positions: torch.Tensor, pos_b: int, pos_n: int, rotary: Rotary, back: int) -> torch.Tensor:
+    """x (its last dimension contiguous) turned, differentiably where x is."""
+    if _differentiated(x):
+        return _Rotate.apply(x, positions, pos_b, pos_n, rotary, back)
+    out = _empty(x)
+    _launch(x, positions, pos_b, pos_n, rotary, back, out)
+    return out
+
+
 class _Rotate(torch.autograd.Function):
-    """Turning by the positions, or back; the gradient is the other one."""
+    """Turning by the positions, or back; the gradient is the other one, and the
+    tangent of x is turned as x is."""
 
     @staticmethod
     def forward(ctx, x, positions, pos_b, pos_n, rotary, back):
         out = _empty(x)
         _launch(x, positions, pos_b, pos_n, rotary, back, out)
         ctx.save_for_backward(positions)
-        ctx.more = (pos_b, pos_n, rotary, 1 - back)
+        ctx.save_for_forward(positions)
+        ctx.more = (pos_b, pos_n, rotary)
+        ctx.back = back
         return out
 
     @staticmethod
     def backward(ctx, grad):
         positions, = ctx.saved_tensors
-        grad = _rows(grad)
-        if torch.is_grad_enabled() and grad.requires_grad:
-            out = _Rotate.apply(grad, positions, *ctx.more)
-        else:
-            out = _empty(grad)
-            _launch(grad, positions, *ctx.more, out)
-        return out, None, None, None, None, None
+        return _turned(_rows(grad), positions, *ctx.more, 1 - ctx.back), None, None, None, None, None
+
+    @staticmethod
+    def jvp(ctx, tangent, *_):
+        positions, = ctx.saved_tensors
+        return _turned(_rows(tangent), positions, *ctx.more, ctx.back)
 
 
 def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -185,7 +205,8 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Option
     pairs turned by the tokens' positions: contiguous [B, H, N, d].
 
     positions: int32 [N] or [B, N], with several axes [N, axes] or
-    [B, N, axes].  Differentiable in x (not with `out`), any number of times.
+    [B, N, axes].  Differentiable in x (not with `out`), any number of times,
+    backward and in forward mode.
 
     To capture a backward pass into a CUDA graph while an eager graph of the same
     leaf lives, run the eager one on the capturing stream: torch ties a leaf's
@@ -197,13 +218,10 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Option
     pos_b, pos_n = _position_strides(positions, B, N, len(rotary.axes), x.device)
     if x.stride(3) != 1 and d > 1:
         raise ValueError("the last dimension of x must be contiguous")
-    if torch.is_grad_enabled() and x.requires_grad:
-        if out is not None:
-            raise ValueError("rotate with a gradient writes its own output: leave `out` away")
-        return _Rotate.apply(x, positions, pos_b, pos_n, rotary, 0)
     if out is None:
-        out = _empty(x)
-    else:
-        api._check_tensor(out, "out", x.shape, x.dtype, x.device)
+        return _turned(x, positions, pos_b, pos_n, rotary, 0)
+    if _differentiated(x):
+        raise ValueError("rotate with a gradient writes its own output: leave `out` away")
+    api._check_tensor(out, "out", x.shape, x.dtype, x.device)
     _launch(x, positions, pos_b, pos_n, rotary, 0, out)
     return out

@@ -1,11 +1,14 @@
 """Rotary positions where they can go wrong beside the ordinary: numbers that are
-not finite in the part of a head that stays."""
+not finite in the part of a head that stays, and forward-mode derivatives."""
 import math
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 import sparse_attention_diffusion_mcs_b200 as mcs
+from tests.cache_util import turned
+from tests.test_gpu_rotary import check
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +46,41 @@ def test_numbers_that_stay_keep_their_bits(dtype, d, dims, layout):
     dx, = torch.autograd.grad(mcs.rotate(leaf, pos, rot), leaf, x)
     assert torch.equal(bits(dx[..., dims:].contiguous()), bits(x[..., dims:].contiguous()))
     assert torch.isfinite(dx[..., :dims]).all()
+
+
+@pytest.mark.parametrize("layout,dims", [("half", 64), ("interleaved", 48)])
+def test_forward_mode(layout, dims):
+    """The map is linear in x: the tangent is turned as x is, with and without a
+    gradient to x, through the gradient too (forward over backward), and a call
+    that could not carry a tangent is refused."""
+    rot = mcs.Rotary(64, dims=dims, layout=layout, magnitude=1.25)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, t, w, u = (torch.randn((2, 3, 9, 64), generator=g, device="cuda") for _ in range(4))
+    pos = torch.randint(0, 9000, (2, 9), generator=g, device="cuda", dtype=torch.int32)
+    p = pos[..., None]
+    for leaf in (x, x.clone().requires_grad_(True)):
+        with fwd.dual_level():
+            y, dy = fwd.unpack_dual(mcs.rotate(fwd.make_dual(leaf, t), pos, rot))
+            assert dy is not None
+            check(y.detach(), turned(x, p, rot), torch.float32)
+            check(dy.detach(), turned(t, p, rot), torch.float32)
+    with fwd.dual_level(), torch.no_grad():
+        dy = fwd.unpack_dual(mcs.rotate(fwd.make_dual(x, t), pos, rot)).tangent
+        check(dy, turned(t, p, rot), torch.float32)
+    strided = torch.randn((2, 9, 64, 3), generator=g, device="cuda").permute(0, 3, 1, 2)   # a tangent of any layout
+    with fwd.dual_level():
+        dy = fwd.unpack_dual(mcs.rotate(fwd.make_dual(x, strided), pos, rot)).tangent
+        check(dy, turned(strided, p, rot), torch.float32)
+    # the gradient's derivative along a tangent of what comes back
+    leaf = x.clone().requires_grad_(True)
+    with fwd.dual_level():
+        y = mcs.rotate(leaf, pos, rot)
+        dx, = torch.autograd.grad(y, leaf, fwd.make_dual(w, u))
+        dx, ddx = fwd.unpack_dual(dx)
+        check(dx, turned(w, p, rot, back=True), torch.float32)
+        assert ddx is not None
+        check(ddx, turned(u, p, rot, back=True), torch.float32)
+    with fwd.dual_level(), pytest.raises(ValueError):
+        mcs.rotate(fwd.make_dual(x, t), pos, rot, out=torch.empty_like(x))
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda z: mcs.rotate(z, pos, rot), (x,), (t,))
