@@ -18,12 +18,12 @@ import torch
 
 from . import api
 from ._lib import McsCache, lib
-from .rotary import Rotary, _check_rotary, _position_strides, _run
+from .rotary import Rotary, _check_rotary, _Handle, _position_strides, _run
 
 _I64x3 = ctypes.c_int64 * 3
 
 
-class KVCache:
+class KVCache(_Handle):
     """The cache's buffers: k_pages, v_pages float8_e4m3fn [n_pages, H, page, d],
     k_scale, v_scale float32 [n_pages, H], page_table int32 [B, max_pages].
     Token j of sequence b is slot j % page of page page_table[b, j // page].
@@ -54,12 +54,7 @@ class KVCache:
         self._c = McsCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                            page_table.data_ptr(), n_pages, max_pages, B, H, page, d)
         self._ref = ctypes.byref(self._c)
-
-    def __setattr__(self, name, value):
-        # the library holds the buffers' addresses: another tensor under the name would not be seen
-        if name in self.__dict__:
-            raise AttributeError(f"{name} belongs to the cache: change it in place, or make another KVCache")
-        super().__setattr__(name, value)
+        self._hold()
 
     @property
     def capacity(self) -> int:

@@ -37,7 +37,27 @@ def _run(name: str, device, *args) -> None:
         check(code, name)
 
 
-class Rotary:
+class _Handle:
+    """What the library holds the addresses of: another tensor under the name would
+    not be seen, and the old one's memory would be read after it is freed."""
+
+    _held = frozenset()
+
+    def _hold(self):
+        self._held = frozenset((*self.__dict__, "_held"))
+
+    def __setattr__(self, name, value):
+        if name in self._held:
+            raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        if name in self._held:
+            raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+        super().__delattr__(name)
+
+
+class Rotary(_Handle):
     """Which numbers of a head of size d turn with the position, and how fast.
 
     dims: how many (from the first; even), default all d.
@@ -53,6 +73,7 @@ class Rotary:
         `original` positions: from `high` turns on it stays, up to `low` it is
         divided by factor, linear in between.
     magnitude: factor on the rotated numbers.
+    A rotary is fixed: for other numbers make another one.
     """
 
     def __init__(self, d: int, dims: Optional[int] = None, base: float = 10000.0, layout: str = "half",
@@ -83,6 +104,7 @@ class Rotary:
         self._c = McsRotary(self.turns.data_ptr(), self.axis.data_ptr(), dims // 2, int(layout == "interleaved"),
                             len(axes), float(magnitude))
         self._ref = ctypes.byref(self._c)
+        self._hold()
 
 
 def _frequencies(m: int, base: float, scaling: Optional[Tuple]):
