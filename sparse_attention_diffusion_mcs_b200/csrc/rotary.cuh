@@ -5,11 +5,14 @@
 //
 // Angles: f is held as the 64-bit fraction of a turn F = round(f / 2pi * 2^64).
 // pos * F mod 2^64 is then the phase, exact for every 32-bit position (the
-// product wraps whole turns away; F's own rounding moves it by less than
-// pos * 2^-65 turns), so far positions lose nothing and no table of angles is
-// read.  The phase's top 32 bits are split into a quarter turn and the rest, at
-// most an eighth of a turn, whose sine and cosine are polynomials (turn_sincos):
-// off by 1.1e-7 at most, in about half the instructions of sincospif.
+// product wraps whole turns away; F's own rounding moves it by at most
+// |pos| * 2^-65 turns), so far positions lose nothing and no table of angles is
+// read.  The phase's top 32 bits (what is cut off is less than 1.5e-9 rad) are
+// split into a quarter turn and the rest, at most an eighth of a turn, whose sine
+// and cosine are polynomials (turn_sincos): off by 1.1e-7 at most, in about half
+// the instructions of sincospif.  Correct rounding would be off by 3e-8; a pair is
+// off by 2.9e-7 of its length in all, which 16-bit outputs do not see (2^-9) and
+// fp32 ones as their last two bits.
 //
 // The kernel is bound by memory: every number is read and written once.  A
 // thread owns 16 numbers of one token (8 pairs, two 16-byte vectors for 16-bit

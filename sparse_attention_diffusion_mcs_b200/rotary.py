@@ -93,7 +93,7 @@ class Rotary(_Handle):
         self.scaling, self.magnitude = scaling, float(magnitude)
         self.frequencies = [f for m in axes for f in _frequencies(m, float(base), scaling)]
         # fractions of a turn per position, times 2^64, kept in int64's bits
-        turns = [round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64 for f in self.frequencies]
+        turns = [_turns(f) % 2 ** 64 for f in self.frequencies]
         turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
         axis = [a for a, m in enumerate(axes) for _ in range(m)]
         # one copy to the device: the turns' 64-bit numbers, then the axes' 32-bit ones
@@ -105,6 +105,17 @@ class Rotary(_Handle):
                             len(axes), float(magnitude))
         self._ref = ctypes.byref(self._c)
         self._hold()
+
+
+# pi * 10^59; in 53 bits the fractions below would be off by hundreds, which far positions multiply
+_PI = 314159265358979323846264338327950288419716939937510582097494
+
+
+def _turns(f: float) -> int:
+    """round(f / 2 pi * 2^64), in whole numbers."""
+    num, den = f.as_integer_ratio()
+    num, den = num * 2 ** 64 * 10 ** 59, den * 2 * _PI
+    return (2 * num + den) // (2 * den)
 
 
 def _frequencies(m: int, base: float, scaling: Optional[Tuple]):

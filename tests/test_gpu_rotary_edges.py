@@ -1,13 +1,16 @@
 """Rotary positions where they can go wrong beside the ordinary: numbers that are
-not finite in the part of a head that stays, and forward-mode derivatives."""
+not finite in the part of a head that stays, forward-mode derivatives, and far
+positions against an exact phase."""
 import math
+from decimal import Decimal
+from fractions import Fraction
 
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
 
 import sparse_attention_diffusion_mcs_b200 as mcs
-from tests.cache_util import turned
+from tests.cache_util import F64, turned
 from tests.test_gpu_rotary import check
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +87,46 @@ def test_forward_mode(layout, dims):
         mcs.rotate(fwd.make_dual(x, t), pos, rot, out=torch.empty_like(x))
     with pytest.raises(RuntimeError):
         torch.func.jvp(lambda z: mcs.rotate(z, pos, rot), (x,), (t,))
+
+
+# 2 pi to 60 digits (the decimal expansion of pi)
+TWO_PI = 2 * Fraction(Decimal("3.14159265358979323846264338327950288419716939937510582097494"))
+
+
+def exactly_turned(x, pos, rotary):
+    """The rotation with every angle reduced in whole numbers: the turns that f
+    (the rotary's own frequency) makes, less the whole ones, to 64 bits."""
+    x = x.detach().to(F64).cpu().clone()
+    p = rotary.dims // 2
+    for i in range(p):
+        j, k = (i, p + i) if rotary.layout == "half" else (2 * i, 2 * i + 1)
+        turn = Fraction(rotary.frequencies[i]) / TWO_PI
+        angle = torch.tensor([2 * math.pi * float(int(n) * turn % 1) for n in pos.tolist()], dtype=F64)
+        c, s = torch.cos(angle), torch.sin(angle)
+        a, b = x[..., j].clone(), x[..., k].clone()
+        x[..., j], x[..., k] = a * c - b * s, a * s + b * c
+    return x
+
+
+@pytest.mark.parametrize("layout,dims", [("half", 128), ("interleaved", 128), ("half", 22)])
+def test_far_positions_against_an_exact_phase(layout, dims):
+    """Every 32-bit position.  Of a pair (a, b), fp32 throughout: the phase is cut to
+    2^-32 turns (1.5e-9 rad) and the table's fraction is off by pos * 2^-65 turns
+    (less still); sine and cosine are off by 1.1e-7 each (the polynomials), 1.6e-7
+    of the pair's length together; one product and the sum are rounded, 2^-24 of
+    that length each, 1.2e-7, the second being the output's own.  2.9e-7 in all."""
+    rot = mcs.Rotary(128, dims=dims, layout=layout, base=500000.0)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    far = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, -2 ** 30 - 77, 2 ** 24 + 1, 123456789, 0, 1, -1, 131071]
+    pos = torch.tensor(far, dtype=torch.int32, device="cuda")
+    x = torch.randn((1, 3, len(far), 128), generator=g, device="cuda")
+    ref = exactly_turned(x, pos, rot)
+    got = mcs.rotate(x, pos, rot).cpu().to(F64)
+    p = dims // 2
+    a, b = (x[..., :p], x[..., p:dims]) if layout == "half" else (x[..., 0:dims:2], x[..., 1:dims:2])
+    length = torch.hypot(a, b).cpu().to(F64)
+    err = (got - ref).abs()
+    e0, e1 = (err[..., :p], err[..., p:dims]) if layout == "half" else (err[..., 0:dims:2], err[..., 1:dims:2])
+    tol = 2.9e-7 * length
+    assert (e0 <= tol).all() and (e1 <= tol).all()
+    assert torch.equal(got[..., dims:], x[..., dims:].cpu().to(F64))

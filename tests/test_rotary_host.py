@@ -1,6 +1,8 @@
 """Rotary's tables on the host: the library holds their addresses, so they cannot
-be rebound."""
+be rebound, and the turns are the nearest 64-bit fractions."""
 import copy
+from decimal import Decimal
+from fractions import Fraction
 
 import pytest
 import torch
@@ -31,3 +33,19 @@ def test_a_cache_keeps_its_buffers():
     with pytest.raises(AttributeError):
         del cache.page_table
     assert cache._c.page_table == cache.page_table.data_ptr()
+
+
+# pi to 60 digits
+PI = Fraction(Decimal("3.14159265358979323846264338327950288419716939937510582097494"))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(base=500000.0, layout="interleaved"), dict(axes=(22, 21, 21)),
+                                dict(scaling=("linear", 3.0)), dict(scaling=("ntk", 7.0)), dict(base=1.01),
+                                dict(scaling=("bands", 8.0, 1.0, 32.0, 8192)), dict(base=0.001), dict(base=1e30)])
+def test_turns_are_the_nearest_fractions(kw):
+    """round(f / 2 pi * 2^64) mod 2^64 of each frequency: off by half at most, so a
+    position p's phase by |p| 2^-65 turns (in 53 bits it was off by hundreds)."""
+    rot = mcs.Rotary(128, device="cpu", **kw)
+    for f, turns in zip(rot.frequencies, rot.turns.tolist()):
+        off = (Fraction(f) / (2 * PI) * 2 ** 64 - turns) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= Fraction(1, 2) + Fraction(1, 10 ** 6)
