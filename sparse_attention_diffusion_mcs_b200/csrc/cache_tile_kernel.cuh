@@ -8,7 +8,9 @@
 // Q.K^T runs in 8 bits straight from the cache's bytes.  A bf16 number has 8
 // significant bits, an e4m3 number 4: with its row scaled so that the largest
 // magnitude lies in [2^7, 2^8), q is hi + lo with hi = e4m3(q), lo = e4m3(q - hi),
-// exact down to 2^-10 of the row's largest and off by at most 2^-18 of it below.
+// exact from 2^-2 on, where lo is a multiple of e4m3's smallest step, 2^-9, and off
+// by at most half that step below: exact down to 2^-9 of the row's largest at
+// worst, and off by at most 2^-17 of it below.
 // Two 8-bit products (hi, then lo) cost what one 16-bit product costs, and no
 // key is converted.
 // P.V runs in fp16: the weights need more than e4m3's 4 bits, and a weight

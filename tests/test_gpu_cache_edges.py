@@ -1,13 +1,13 @@
 """The cache where it can go wrong beside the ordinary: numbers that are not
-finite in the part of a key that stays."""
+finite in the part of a key that stays, and how exact attention is."""
 import math
 
 import pytest
 import torch
 
 import sparse_attention_diffusion_mcs_b200 as mcs
-from tests.cache_util import F64, tokens
-from tests.test_gpu_cache import i32
+from tests.cache_util import F64, attended, held, random_cache, tokens
+from tests.test_gpu_cache import CASES, WIDE, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,69 @@ def test_an_infinity_in_the_part_of_a_key_that_stays(dims):
     assert torch.equal(ka, kb)
     Q = torch.randn((1, 2, 5, 64), generator=g).to(torch.bfloat16)
     assert torch.isfinite(mcs.cache_attention(Q.cuda(), b, i32(40))).all()
+
+
+def score_error(Q, cache, E, scale=None):
+    """How far a row's scores may be off: E of cache_util (fp32 sums of d products), and
+    for blocks of many rows the queries' two 8-bit parts, off by at most 2^-17 of
+    the row's largest number each: 2^-17 max|q| sum|k| of the largest key."""
+    scale = 1 / math.sqrt(Q.shape[-1]) if scale is None else scale
+    keys = torch.nan_to_num(held(cache)[0].abs(), 0.0).sum(-1).max()
+    return E + scale * 2.0 ** -17 * Q.to(F64).abs().amax(-1) * keys
+
+
+def bound(Q, cache, lengths, A, E, scale=None):
+    """How far a number may be from the definition, beside its own rounding, in
+    units of the weighted magnitudes A = sum_j p_j |v_j| of its row:
+    - a weight is rounded to fp16, 2^-11 of it (the sum they are divided by is not
+      rounded): 2^-11;
+    - a score's error moves a weight, and the sum: twice;
+    - the exponential (2^-22), its argument's rounding (up to 2^7: 2^-17, twice): 2^-16;
+    - fp32 sums over up to n / 16 steps of 16 keys: (n / 16) 2^-23;
+    and a weight below fp16's normal range is off by 2^-25 where the row's largest
+    is 2^6 or more: n of them by n 2^-31 of the row's largest term, which is at
+    most n 2^-31 * max|v| (numbers and scales of these caches are alike over the pages)."""
+    n = max(max(lengths), 1)
+    a = 2.0 ** -11 + 2 * score_error(Q, cache, E, scale) + 2.0 ** -16 + n / 16 * 2.0 ** -23
+    return a[..., None] * A + n * 2.0 ** -31 * torch.nan_to_num(held(cache)[1].abs(), 0.0).max()
+
+
+def assert_within(got, ref, extra):
+    got = got.cpu().to(F64)
+    assert torch.isfinite(got).all()
+    worst = ((got - ref).abs() / (2.0 ** -8 * ref.abs() + extra + 1e-30)).max().item() if ref.numel() else 0.0
+    assert worst <= 1.0, f"off by {worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention_is_as_exact_as_its_weights(case, places):
+    B, Hq, H, Nq, d, page, lengths, causal, counts = CASES[case]
+    cache = random_cache(B, H, lengths, d, page, seed=Nq + 1, places=places)
+    g = torch.Generator().manual_seed(10)
+    Q = (torch.randn((B, Hq, Nq, d), generator=g) * 1.5).to(torch.bfloat16)
+    Q[..., ::3] *= 0.01
+    ref, _, A, E = attended(Q, cache, lengths, causal, counts)
+    O = mcs.cache_attention(Q.cuda(), cache, i32(*lengths), causal=causal, counts=None if counts is None else i32(*counts))
+    assert_within(O, ref, bound(Q, cache, lengths, A, E))
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("Nq,n,d", [(1, 6, 64), (16, 6, 128), (40, 10, 64), (300, 6, 128), (300, 2, 64), (300, 400, 64)])
+def test_values_that_cancel(Nq, n, d, places):
+    """Neighbouring tokens with opposite values and scores close to each other:
+    the output is small beside the weighted magnitudes, so the weights' own
+    rounding shows (weights of 8 significant bits are off by several times the bound)."""
+    B, H = 1, 8
+    cache = random_cache(B, H, [n], d, 128, seed=3, spread=0.0, places=places)
+    k, v = cache.k_pages.float(), cache.v_pages.float()
+    k *= 2.0 ** -4
+    v[:, :, 1::2] = -v[:, :, ::2]
+    for to, x in ((cache.k_pages, k), (cache.v_pages, v)):
+        to.view(torch.uint8).copy_(x.to(torch.float8_e4m3fn).view(torch.uint8))
+    g = torch.Generator().manual_seed(10)
+    Q = torch.randn((B, H, Nq, d), generator=g).to(torch.bfloat16)
+    ref, _, A, E = attended(Q, cache, [n], False)
+    assert (ref.abs().mean() < 0.2 * A.mean()).item()
+    O = mcs.cache_attention(Q.cuda(), cache, i32(n))
+    assert_within(O, ref, bound(Q, cache, [n], A, E))
