@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
       for (int i = 0; i < SEG * 8; ++i) am = max(am, max((x[i] << 1) & 0xFFFEu, (x[i] >> 15) & 0xFFFEu));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
+      const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 126);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       rowf[u] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       if (am >> 8 == 255) rowf[u] = __uint_as_float(0x7FC00000u);   // a query that is not finite: NaN
@@ -479,7 +479,10 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
     float *wo = reinterpret_cast<float *>(smem + C::OFF_WO);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      float s = l[u];
+      // sums of products stay below 2^17 and scales are at most 2^60: from 2^48 on scores
+      // may leave fp32.  Above it they make NaN; a row with keys and all its scores below is NaN too.
+      const bool lost = rowf[u] >= 0x1p48f && m[u] == -INFINITY && lim[u] > sg.t0 * BN + warp * 32;
+      float s = lost ? NAN : l[u];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       if (t == 0)

@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
             for (int k = 0; k < 4; ++k) am = max(am, max((x[k] << 1) & 0xFFFEu, (x[k] >> 15) & 0xFFFEu));
 #pragma unroll
             for (int o = LPR / 2; o; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-            const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 100);
+            const int e = min(max(static_cast<int>(am >> 8) - 127, -100), 127);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
             const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
             if (qc == 0) rf[qr] = am >> 8 == 255 ? __uint_as_float(0x7FC00000u) : down;   // a query that is not finite: NaN
@@ -619,6 +619,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           tc_fence_before();
           warp_arrive(b_p(half));
         }
+        // sums of products stay below 2^24 and scales are at most 2^60: from 2^40 on scores
+        // may leave fp32.  Above it they make NaN; a row with keys and all its scores below is NaN too.
+        if (rowf >= 0x1p40f && m_run == -INFINITY && lim > (sg.t0 + skip) * BN) l_run = NAN;
         if (ok && !mbar_wait_warp(b_o(half), n_part & 1, a.wait_ns, abort_flag)) ok = false;
         ++n_part;
         if (!ok) break;

@@ -1,5 +1,5 @@
 """The cache where it can go wrong beside the ordinary: numbers that are not
-finite in the part of a key that stays, and how exact attention is."""
+finite in the part of a key that stays, how exact attention is, and queries far out."""
 import math
 
 import pytest
@@ -104,3 +104,47 @@ def test_values_that_cancel(Nq, n, d, places):
     assert (ref.abs().mean() < 0.2 * A.mean()).item()
     O = mcs.cache_attention(Q.cuda(), cache, i32(n))
     assert_within(O, ref, bound(Q, cache, [n], A, E))
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("Nq", [1, 40])
+@pytest.mark.parametrize("power", [-90, -60, 90, 105, 120, 127])
+def test_queries_of_any_finite_size(power, Nq, places):
+    """Small keys bring the scores back to an ordinary size (scales of 2^-60, and
+    the softmax's scale for the rest): rows of huge and tiny numbers are as
+    exact as others."""
+    d, n = 64, 200
+    cache = random_cache(1, 2, [n], d, 32, seed=4, spread=0.0, places=places)
+    down = min(max(-power, -60), 60)
+    cache.k_scale.fill_(2.0 ** (down - 6))
+    scale = 2.0 ** (-power - down - 3)
+    if down - 6 < -60:
+        cache.k_scale.fill_(2.0 ** -60)
+        scale = 2.0 ** (60 - 6 - power - 3)
+    g = torch.Generator().manual_seed(9)
+    Q = torch.randn((1, 2, Nq, d), generator=g).clamp(-1.9, 1.9) * 2.0 ** power
+    Q[..., ::3] *= 0.01
+    Q = Q.to(torch.bfloat16)
+    assert torch.isfinite(Q).all()
+    ref, lse, A, E = attended(Q, cache, [n], False, scale=scale)
+    O, got = mcs.cache_attention(Q.cuda(), cache, i32(n), scale=scale, return_lse=True)
+    assert_within(O, ref, bound(Q, cache, [n], A, E, scale))
+    assert ((got.cpu().to(F64) - lse).abs() <= score_error(Q, cache, E, scale) + 1e-5 + 1e-6 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_scores_beyond_fp32_give_nan(Nq, sign, places):
+    """All above it, all below it: NaN, and never zeros; other rows are not reached."""
+    n = 200
+    cache = random_cache(1, 1, [n], 64, 32, seed=4, spread=0.0, places=places)
+    k = cache.k_pages.float().abs().clamp(min=1.0)
+    cache.k_pages.view(torch.uint8).copy_(k.to(torch.float8_e4m3fn).view(torch.uint8))
+    cache.k_scale.fill_(2.0 ** 60)
+    Q = torch.full((1, 2, Nq, 64), 2.0 ** -70, dtype=torch.bfloat16, device="cuda")
+    Q[0, 1] = sign * 2.0 ** 120
+    for causal in (False, True):
+        O, lse = mcs.cache_attention(Q, cache, i32(n), causal=causal, return_lse=True)
+        assert torch.isfinite(O[0, 0]).all() and torch.isfinite(lse[0, 0]).all()
+        assert O[0, 1].isnan().all() and lse[0, 1].isnan().all()
