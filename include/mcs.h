@@ -399,8 +399,11 @@ mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, cons
 
 /* A paged cache of keys and values in e4m3 (e4m3fn), all device memory owned
  * by the caller.  Token j of sequence b lies in page page_table[b, j / page],
- * slot j % page.  A stored number stands for e4m3 * scale of its page and head
- * (scales are positive; append writes powers of two).  Table entries behind a
+ * slot j % page.  A stored number stands for e4m3 * scale of its page and head.
+ * append writes scales that are powers of two from 2^-60 to 2^60; others may be
+ * a caller's: of keys 0 to 2^60, of values 2^-60 to 2^60, or 0.  Attention
+ * leaves a page with another scale out, for its head, and records
+ * MCS_ERR_BAD_META.  Table entries behind a
  * sequence's last page are never read.  An entry outside [0, n_pages) that is
  * needed records MCS_ERR_BAD_META in the status word and is never followed:
  * append writes nothing there, read gives zeros, attention leaves the page's

@@ -27,6 +27,9 @@ class KVCache(_Handle):
     """The cache's buffers: k_pages, v_pages float8_e4m3fn [n_pages, H, page, d],
     k_scale, v_scale float32 [n_pages, H], page_table int32 [B, max_pages].
     Token j of sequence b is slot j % page of page page_table[b, j // page].
+    A number stands for e4m3 * scale of its page and head.  Scales of a caller's own
+    are 0 to 2^60 for keys, 2^-60 to 2^60, or 0, for values; attention leaves out,
+    and records (last_device_status), a page whose scale is none of these.
 
     Calls work on these very buffers: change their contents in place (new pages
     in page_table, for instance); for other buffers make another KVCache."""

@@ -233,6 +233,13 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
         }
       };
       fetch_scales(pid, ks, vs);
+      auto check_scales = [&]() {
+        if (pid >= 0 && !scales_fit(ks, vs)) {
+          record_status(a.status, kStatusBadMeta);
+          pid = -1;
+        }
+      };
+      check_scales();
       const int gpb = cv.page / 16;                    // groups per page (a page is at most a tile)
       for (int tb = sg.t0; tb < sg.t1 && ok; tb += 4) {
         const int npid = fetch_page(8 * (tb + 4) + lane);
@@ -243,14 +250,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
           const int gl = 8 * (t - tb);                 // lane of the tile's first group
           ok = mbar_wait_warp(b_empty(s), ((it / NS) & 1) ^ 1, a.wait_ns, abort_flag);
           if (!ok) break;
-          if (lane >= gl && lane < gl + 8) {
-            float4 f;
-            f.x = ks;
-            f.y = pid >= 0 ? __log2f(vs) : -INFINITY;
-            f.z = pid >= 0 ? 1.f / vs : 0.f;
-            f.w = 0.f;
-            *reinterpret_cast<float4 *>(smem + C::OFF_SC + (s * 8 + lane - gl) * 16) = f;
-          }
+          if (lane >= gl && lane < gl + 8)
+            *reinterpret_cast<float4 *>(smem + C::OFF_SC + (s * 8 + lane - gl) * 16) = page_factors(pid >= 0, ks, vs, 0.f);
           // the first lane of each page's groups loads it
           const bool mine = lane >= gl && lane < gl + 8 && (lane - gl) % gpb == 0 && pid >= 0;
           const unsigned who = __ballot_sync(0xffffffffu, mine);
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
         pid = npid;
         ks = nks;
         vs = nvs;
+        check_scales();
       }
     }
     if (!ok && lane == 0 && !*abort_flag) {
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
         const uint8_t *vb = kb + C::TILE;
         const float4 *scp = reinterpret_cast<const float4 *>(smem + C::OFF_SC) + s * 8 + warp * 2;
         const float4 sc0 = scp[0], sc1 = scp[1];
-        const bool clean = key0 + 32 <= all && sc0.y > -INFINITY && sc1.y > -INFINITY;
+        const bool clean = key0 + 32 <= all && sc0.y > kHasValues && sc1.y > kHasValues;
         // ---- scores of 32 keys
         float sc[4][4];
 #pragma unroll
@@ -452,9 +454,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
               const uint2 z = *reinterpret_cast<const uint2 *>(vb + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16) + (g & 1) * 8);
               w[q] = make_uint4(z.x, z.y, 0, 0);
             }
-            // what lies behind the last token, or was never loaded, may be any bits
+            // what lies behind the last token, or was never loaded, or has a scale of 0, may be any bits
             const float lv = ii ? sc1.y : sc0.y;
-            if (!clean && !(key0 + r < kmax && lv > -INFINITY)) w[q] = make_uint4(0, 0, 0, 0);
+            if (!clean && !(key0 + r < kmax && lv > kHasValues)) w[q] = make_uint4(0, 0, 0, 0);
           }
           const uint32_t x0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, x1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
           const uint32_t x2[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, x3[4] = {w[3].x, w[3].y, w[3].z, w[3].w};

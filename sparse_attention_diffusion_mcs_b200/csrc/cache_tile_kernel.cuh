@@ -273,6 +273,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
       int pid = fetch_page(8 * sg.t0 + lane);
       float ks, vs;
       fetch_scales(pid, ks, vs);
+      auto check_scales = [&]() {
+        if (pid >= 0 && !scales_fit(ks, vs)) {
+          record_status(a.status, kStatusBadMeta);
+          pid = -1;
+        }
+      };
+      check_scales();
       for (int tb = sg.t0; tb < end && ok; tb += 4) {
         const int npid = fetch_page(8 * (tb + 4) + lane);
         float nks, nvs;
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
         for (int t = tb; t < min(tb + 4, end); ++t, ++it) {
           const int gl = 8 * (t - tb);                 // lane of the tile's first group
           const bool in = lane >= gl && lane < gl + 8;
-          const unsigned good = __ballot_sync(0xffffffffu, in && pid >= 0);
+          const unsigned good = __ballot_sync(0xffffffffu, in && pid >= 0 && vs > 0.f);
           // the first lane of each page's groups loads it
           const bool mine = in && (lane - gl) % gpb == 0 && pid >= 0;
           const uint32_t tx = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
@@ -290,8 +297,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           if (!ok) break;
           if (in)
             *reinterpret_cast<float4 *>(smem + C::OFF_SC + ((it % NSC) * 8 + lane - gl) * 16) =
-                make_float4(ks, pid >= 0 ? __log2f(vs) : -INFINITY, pid >= 0 ? 1.f / vs : 0.f,
-                            __popc(good) == 8 ? 1.f : 0.f);
+                page_factors(pid >= 0, ks, vs, __popc(good) == 8 ? 1.f : 0.f);
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(b_sc(it));
@@ -311,6 +317,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
         pid = npid;
         ks = nks;
         vs = nvs;
+        check_scales();
       }
     }
     if (!ok && lane == 0) give_up();
@@ -352,12 +359,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           uint4 w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(src + from + (i0 + i) * RSTEP * D);
-          // what lies behind the last key that is seen, or was never loaded, may be any bits
+          // what lies behind the last key that is seen, or was never loaded, or has a scale of 0, may be any bits
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = key + (i0 + i) * RSTEP;
-              if (!(t * BN + r < sg.kmax && sc[r >> 4].y > -INFINITY)) w[i] = make_uint4(0, 0, 0, 0);
+              if (!(t * BN + r < sg.kmax && sc[r >> 4].y > kHasValues)) w[i] = make_uint4(0, 0, 0, 0);
             }
           }
 #pragma unroll

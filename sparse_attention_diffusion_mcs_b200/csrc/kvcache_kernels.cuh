@@ -37,6 +37,19 @@ struct CacheView {
   int n_pages, max_pages, H, page, d;
 };
 
+// Scales that attention takes: of keys 0 to 2^60, of values 2^-60 to 2^60, or 0 (the
+// values are 0, whatever the bytes).  Others are recorded and the page is left out.
+__device__ __forceinline__ bool scales_fit(float ks, float vs) {
+  return ks >= 0.f && ks <= 0x1p60f && (vs == 0.f || (vs >= 0x1p-60f && vs <= 0x1p60f));
+}
+// What attention reads of a page: (ks, log2 vs, 1 / vs, w); log2 vs is -inf where
+// there is none, and -61 for a vs of 0: below kHasValues the bytes of V count as 0.
+constexpr float kHasValues = -60.5f;
+__device__ __forceinline__ float4 page_factors(bool have, float ks, float vs, float w) {
+  const float v = vs == 0.f ? 0x1p-61f : vs;
+  return make_float4(ks, have ? __log2f(v) : -INFINITY, have ? 1.f / v : 0.f, w);
+}
+
 // two fp32 numbers to two e4m3 bytes (lo in the low byte), to nearest, +-inf and
 // what is out of range to +-448, NaN to NaN
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

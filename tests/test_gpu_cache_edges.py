@@ -1,5 +1,6 @@
 """The cache where it can go wrong beside the ordinary: numbers that are not
-finite in the part of a key that stays, how exact attention is, and queries far out."""
+finite in the part of a key that stays, how exact attention is, and queries and
+scales far out."""
 import math
 
 import pytest
@@ -148,3 +149,60 @@ def test_scores_beyond_fp32_give_nan(Nq, sign, places):
         O, lse = mcs.cache_attention(Q, cache, i32(n), causal=causal, return_lse=True)
         assert torch.isfinite(O[0, 0]).all() and torch.isfinite(lse[0, 0]).all()
         assert O[0, 1].isnan().all() and lse[0, 1].isnan().all()
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("Nq,d,page", [(1, 64, 16), (5, 128, 64), (40, 64, 32), (300, 128, 128)])
+def test_scales_of_a_callers_own(Nq, d, page, places):
+    """Scales that are no powers of two; key scales of zero (scores of zero); value
+    scales of zero: the page's values are zero, whatever its bytes, and its
+    weights count.  (lse: the scores' error, 1e-5 and 1e-6 of it for the sum's
+    rounding, log2 of a scale 2^-22 of 7: 1e-5 covers it.)"""
+    lengths = [700, 300]
+    cache = random_cache(2, 2, lengths, d, page, seed=8, spread=0.0, places=places)
+    g = torch.Generator().manual_seed(12)
+    for s in (cache.k_scale, cache.v_scale):
+        s.mul_((0.6 + torch.rand(s.shape, generator=g)).cuda())
+    used = [int(p) for p in cache.page_table[cache.page_table >= 0].tolist()]
+    cache.v_scale[used[0], 0] = 0.0
+    cache.v_scale[used[1 % len(used)], :] = 0.0
+    cache.k_scale[used[-1], 1] = 0.0
+    cache.k_scale[used[0], 0] *= 4                       # (weights that would be missed)
+    Q = (torch.randn((2, 4, Nq, d), generator=g) * 1.5).to(torch.bfloat16)
+    for causal in (False, True):
+        ref, lse, A, E = attended(Q, cache, lengths, causal)
+        O, got = mcs.cache_attention(Q.cuda(), cache, i32(*lengths), causal=causal, return_lse=True)
+        assert_within(O, ref, bound(Q, cache, lengths, A, E))
+        got = got.cpu().to(F64)
+        assert ((got - lse).abs() <= score_error(Q, cache, E) + 2e-5 + 1e-6 * lse.abs()).all()
+    # all of a row's values are zero: zeros, and a finite sum
+    cache.v_scale.zero_()
+    O, got = mcs.cache_attention(Q.cuda(), cache, i32(*lengths), return_lse=True)
+    _, lse, _, E = attended(Q, cache, lengths, False)
+    assert (O == 0).all() and ((got.cpu().to(F64) - lse).abs() <= score_error(Q, cache, E) + 2e-5 + 1e-6 * lse.abs()).all()
+    for x in mcs.cache_read(cache, i32(0, 0), 300)[1:]:
+        assert (x == 0).all()
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("Nq", [1, 40])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -1.0, 2.0 ** 61, 2.0 ** -61])
+def test_scales_out_of_range_are_recorded(bad, Nq, places):
+    """A page with such a scale is left out of its head's attention, and recorded, as a bad page is."""
+    cache = random_cache(1, 2, [300], 64, 32, seed=8, spread=0.0, places=places)
+    g = torch.Generator().manual_seed(12)
+    Q = torch.randn((1, 2, Nq, 64), generator=g).to(torch.bfloat16)
+    table = cache.page_table[0].tolist()
+    good_v, good_k = cache.v_scale.clone(), cache.k_scale.clone()
+    ref, _, A, E = attended(Q, cache, [300], False, drop={0: list(range(64, 96))})
+    other, _, A1, E1 = attended(Q, cache, [300], False)
+    for t, good in ((cache.v_scale, good_v), (cache.k_scale, good_k)):
+        if t is cache.k_scale and abs(bad) < 1:
+            continue                                      # a small key scale is one
+        t[table[2], 0] = bad
+        O = mcs.cache_attention(Q.cuda(), cache, i32(300))
+        assert mcs.last_device_status() == 6
+        t.copy_(good)
+        assert_within(O[:, 0], ref[:, 0], bound(Q, cache, [300], A, E)[:, 0])
+        assert_within(O[:, 1], other[:, 1], bound(Q, cache, [300], A1, E1)[:, 1])
+    assert mcs.last_device_status() == 0
