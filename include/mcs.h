@@ -389,8 +389,9 @@ typedef struct {
  *   for B, H, N and 1 for d; any alignment, stride 0 included.
  * positions: int32 [B, N, axes], strides pos_stride_b and pos_stride_n (0 to
  *   repeat), 1 for the axes.  Computed in fp32, rounded once.
- * out: contiguous [B, H, N, d], no overlap with x.  B, H or N of 0: no-op.
- * INVALID_ARG for null pointers, 2 * pairs > d, axes < 1, magnitude <= 0;
+ * out: contiguous [B, H, N, d]; x itself where that is contiguous (in place),
+ *   else nothing of the memory from x's first to its last number.  B, H or N of 0: no-op.
+ * INVALID_ARG for null pointers, 2 * pairs > d, axes < 1, magnitude <= 0, overlap;
  * UNSUPPORTED for another dtype.  Asynchronous.
  */
 mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, const int64_t *strides,
@@ -453,7 +454,7 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
 /*
  * mcs_cache_attention -- O = softmax(scale Q K^T) V over the cache's tokens
  * [0, lengths[b]) of each sequence.
- * Q, O: bf16 [B, Hq, Nq, d], contiguous, 16-byte aligned, no overlap; Hq a
+ * Q, O: bf16 [B, Hq, Nq, d], contiguous, 16-byte aligned, no overlap (INVALID_ARG); Hq a
  *   multiple of H: query head h goes by key head h / (Hq / H).  Nq * Hq / H <= 2^20.
  * lengths: int32 [B]; more than the table holds counts as what it holds and
  *   records MCS_ERR_BAD_META.

@@ -18,7 +18,7 @@ import torch
 
 from . import api
 from ._lib import McsCache, lib
-from .rotary import Rotary, _check_rotary, _Handle, _position_strides, _run
+from .rotary import Rotary, _check_apart, _check_rotary, _Handle, _position_strides, _run
 
 _I64x3 = ctypes.c_int64 * 3
 
@@ -189,6 +189,7 @@ def cache_attention(Q: torch.Tensor, cache: KVCache, lengths: torch.Tensor, caus
         out = torch.empty_like(Q)
     else:
         api._check_tensor(out, "out", Q.shape, torch.bfloat16, cache.device)
+        _check_apart(Q, out, False)
     lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=cache.device) if return_lse else None
     need = lib().mcs_cache_attention_workspace_size(cache._ref, Hq, Nq)
     ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None

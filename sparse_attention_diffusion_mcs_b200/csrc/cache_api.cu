@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/mcs.h"
 #include "cache_rows_kernel.cuh"
@@ -78,6 +79,12 @@ mcs_status check_cache(const mcs_cache *c, CacheView *v) {
   v->page = c->page;
   v->d = c->d;
   return MCS_OK;
+}
+
+// whether [p, p + np) and [q, q + nq) have bytes in common
+bool overlap(const void *p, __int128 np, const void *q, __int128 nq) {
+  const __int128 a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
 }
 
 // ---------------------------------------------------------------- rotate
@@ -243,6 +250,16 @@ mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, cons
   a.N = N;
   a.d = d;
   a.back = back != 0;
+  // out over x: in place only, where every thread reads the numbers it writes first
+  const bool same = x == out && (N == 1 || a.sn == d) && (H == 1 || a.sh == static_cast<long long>(N) * d) &&
+                    (B == 1 || a.sb == static_cast<long long>(H) * N * d);
+  __int128 lo = 0, hi = d;   // the numbers of x: [lo, hi)
+  for (const __int128 reach : {static_cast<__int128>(B - 1) * a.sb, static_cast<__int128>(H - 1) * a.sh,
+                               static_cast<__int128>(N - 1) * a.sn})
+    (reach < 0 ? lo : hi) += reach;
+  const uint8_t *first = static_cast<const uint8_t *>(x) + static_cast<ptrdiff_t>(lo * elt);
+  if (!same && overlap(first, (hi - lo) * elt, out, static_cast<__int128>(B) * H * N * d * elt))
+    return MCS_ERR_INVALID_ARG;
   // 16-byte vectors need whole units of 16 numbers and aligned rows
   const bool vec = d % 16 == 0 && (a.t.interleaved || a.t.pairs % 8 == 0) && aligned16(x) && aligned16(out) &&
                    a.sb * elt % 16 == 0 && a.sh * elt % 16 == 0 && a.sn * elt % 16 == 0;
@@ -348,6 +365,8 @@ mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, in
   const long long n_rows = static_cast<long long>(Nq) * (Hq / a.c.H);
   if (n_rows > (1 << 20)) return MCS_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return MCS_ERR_INVALID_ARG;
+  const __int128 bytes = static_cast<__int128>(cache->B) * Hq * Nq * a.c.d * 2;
+  if (overlap(Q, bytes, O, bytes)) return MCS_ERR_INVALID_ARG;
   if (!(a.status = device_status_word())) return MCS_ERR_CUDA;
   const AttnPlan p = plan_attention(a.c, cache->B, n_rows);
   if (p.ctas) {

@@ -182,6 +182,19 @@ def _launch(x: torch.Tensor, positions: torch.Tensor, pos_b: int, pos_n: int, ro
          pos_b, pos_n, rotary._ref, back, out.data_ptr())
 
 
+def _check_apart(x: torch.Tensor, out: torch.Tensor, in_place: bool) -> None:
+    """out (contiguous, x's shape) shares no memory with the stretch from x's first
+    to its last number, or (in_place) is x itself: threads would read what others
+    have written."""
+    n, apart = x.numel(), out.data_ptr() - x.data_ptr()
+    packed = x.is_contiguous()
+    if n == 0 or in_place and packed and apart == 0:
+        return
+    end = n if packed else sum((m - 1) * s for m, s in zip(x.shape, x.stride())) + 1
+    if -n < apart / x.element_size() < end:
+        raise ValueError("out must not overlap the input")
+
+
 def _rows(x: torch.Tensor) -> torch.Tensor:
     """x with its last dimension contiguous (a gradient may come in any layout)."""
     return x if x.stride(3) == 1 or x.shape[3] == 1 else x.contiguous()
@@ -239,7 +252,8 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Option
 
     positions: int32 [N] or [B, N], with several axes [N, axes] or
     [B, N, axes].  Differentiable in x (not with `out`), any number of times,
-    backward and in forward mode.
+    backward and in forward mode.  `out` may be x itself, contiguous (in place),
+    and must not overlap it otherwise.
 
     To capture a backward pass into a CUDA graph while an eager graph of the same
     leaf lives, run the eager one on the capturing stream: torch ties a leaf's
@@ -256,5 +270,6 @@ def rotate(x: torch.Tensor, positions: torch.Tensor, rotary: Rotary, out: Option
     if _differentiated(x):
         raise ValueError("rotate with a gradient writes its own output: leave `out` away")
     api._check_tensor(out, "out", x.shape, x.dtype, x.device)
+    _check_apart(x, out, True)
     _launch(x, positions, pos_b, pos_n, rotary, 0, out)
     return out
