@@ -471,6 +471,8 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
  *   gives for the same cache, Hq and Nq (0: none needed), this call's own until
  *   it has run on its stream; nothing in it matters before or after.
  * Nq == 0 is a no-op.  Repeats bit for bit.  Asynchronous.
+ * lengths and counts must not change while the call runs: its numbers are then
+ * worth nothing, and MCS_ERR_TIMEOUT may be recorded.
  */
 size_t mcs_cache_attention_workspace_size(const mcs_cache *cache, int Hq, int Nq);
 mcs_status mcs_cache_attention(const mcs_cache *cache, const void *Q, int Hq, int Nq, const int32_t *lengths,

@@ -287,7 +287,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
     const int g = lane >> 2, t = lane & 3;
     bool ok = true;
     int it = 0;
-    while (next(sg)) {
+    // the four warps have barriers between them: all go on to a part, or none
+    auto more = [&]() -> bool { return CLUSTER ? run.left : run.more(sa); };
+    while (group_ok(ok && more()) && next(sg)) {
     const int row0 = sg.block * 16;                 // rows are (token, query head of the group)
     const int kmax = sg.kmax;
     // keys that row i of the item sees: [0, limit)
@@ -557,7 +559,6 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
       }
       if (q + 1 < NT / 4) asm volatile("bar.sync 1, 128;" ::: "memory");
     }
-    if (!group_ok(ok)) break;          // all four warps give up together
     }   // parts
   }
   // ---------------------------------------------------------------------- merge over the cluster

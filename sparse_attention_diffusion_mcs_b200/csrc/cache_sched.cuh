@@ -10,6 +10,10 @@
 // first item and its last -- and writes down where an item goes on, and
 // cache_merge_kernel, launched behind, adds the parts up in the order of the
 // keys.  No atomics: results repeat bit for bit.
+//
+// Lengths are read again and again, here and by the roles of a CTA.  A caller that
+// changes them while a call runs gets numbers that are worth nothing; but every
+// loop is bounded by sizes that the host gave, and every index is in range.
 #pragma once
 
 #include "kvcache_kernels.cuh"
@@ -99,13 +103,14 @@ struct Sched {
     quota = (total + n_cta - 1) / n_cta;
     quota = quota < min_quota ? min_quota : quota;
     const long long u0 = quota * cta;
-    left = total - u0 < quota ? total - u0 : quota;
+    const long long share_of = total - u0 < quota ? total - u0 : quota;
+    left = 0;                                // (unless the run's beginning is found)
     b = h = block = 0;
     off = 0;
-    if (left <= 0) return;
+    if (share_of <= 0) return;
     long long before = 0, mine = 0;          // units before the sequence, and of one of its heads
     if (by_lane) {
-      for (int b0 = 0;; b0 += 32) {          // ends: u0 < total
+      for (int b0 = 0; b0 < s.B; b0 += 32) {   // (found: u0 < total)
         long long v = 0;
         for (int k = 0; b0 + lane < s.B && k < s.n_blocks; ++k) v += units(s, b0 + lane, k);
         const long long sum = warp_scan(v * s.H, lane);
@@ -120,7 +125,7 @@ struct Sched {
         before += __shfl_sync(0xffffffffu, sum, 31);
       }
     } else {
-      for (b = 0;; ++b) {
+      for (b = 0; b < s.B; ++b) {
         const long long v = sequence_units(s, b, lane);
         if (before + v > u0) {
           mine = v / s.H;
@@ -129,10 +134,11 @@ struct Sched {
         before += v;
       }
     }
+    if (mine == 0) return;
     long long r = u0 - before;
     h = static_cast<int>(r / mine);
     r -= h * mine;
-    for (int k0 = 0;; k0 += 32) {            // ends: r < mine
+    for (int k0 = 0; k0 < s.n_blocks; k0 += 32) {   // (found: r < mine)
       const long long v = k0 + lane < s.n_blocks ? units(s, b, k0 + lane) : 0;
       const long long sum = warp_scan(v, lane);
       const unsigned hit = __ballot_sync(0xffffffffu, sum > r);
@@ -140,27 +146,30 @@ struct Sched {
         const int l = __ffs(hit) - 1;
         block = k0 + l;
         off = r - (__shfl_sync(0xffffffffu, sum, l) - __shfl_sync(0xffffffffu, v, l));
-        break;
+        left = share_of;
+        return;
       }
       r -= __shfl_sync(0xffffffffu, sum, 31);
     }
   }
 
+  // whether next() has another part
+  __device__ __forceinline__ bool more(const SchedArgs &s) const { return left > 0 && b < s.B; }
   // the next part of this CTA's run
   __device__ __forceinline__ bool next(const SchedArgs &s, Segment &g) {
-    if (left <= 0) return false;
+    if (!more(s)) return false;
     g.b = b;
     g.h = h;
     g.block = block;
     const int tiles = item(s, b, block, g);
     const long long all = static_cast<long long>(tiles) * g.halves;
-    const long long take = all - off < left ? all - off : left;
+    const long long rest = all > off ? all - off : 0, take = rest < left ? rest : left;
     // tile t is of the CTA that has the unit t * halves
     g.t0 = static_cast<int>((off + g.halves - 1) / g.halves);
     g.t1 = static_cast<int>((off + take + g.halves - 1) / g.halves);
     g.first = off == 0;
     g.whole = g.t0 == 0 && g.t1 == tiles;
-    g.go_on = g.whole ? 0 : static_cast<int>((all - off - take + quota - 1) / quota);
+    g.go_on = g.whole ? 0 : static_cast<int>((rest - take + quota - 1) / quota);
     left -= take;
     off = 0;
     if (++block == s.n_blocks) {
@@ -272,8 +281,9 @@ __device__ __forceinline__ MergeSum merge_parts(const MergeArgs &a, int c, int g
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kMergeThreads, 6) cache_merge_kernel(const __grid_constant__ MergeArgs a) {
   const int c = blockIdx.x;
-  const MergeItem it = a.m.items[c];
+  MergeItem it = a.m.items[c];
   if (it.go_on == 0) return;
+  it.go_on = min(it.go_on, static_cast<int>(gridDim.x) - 1 - c);   // (gridDim.x: the CTAs that computed)
   constexpr int QG = D / 16;                                 // groups of 4 quads
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = it.block * a.rows;
