@@ -123,6 +123,20 @@ struct AttnPlan {
 //   there can be tiles, on blocks of 16 rows.  More rows than 16 read the keys
 //   once a block, but start at once: 20 rows of 16 heads against 8191 tokens take
 //   15.5 us, as one block of 32 rows 26, with the tile kernel 25 and 5 of merge.
+//   Both sides of the two borders, us of a call after a flush, clusters | dealt:
+//   items x tiles an SM, near 28 a second round of clusters begins:
+//     one token, 32 heads on 8 of 128, 32 tiles: 13.8: 28 | 37, 27.7: 41 | 50, 34.6: 61 | 56
+//     one token, 8 heads of 64, 8 tiles: 27.7: 33 | 38, 31.1: 35 | 40, 34.6: 43 | 42
+//     rows of 16 heads of 128, 64 tiles: 20.8: 35 | 53, 27.7: 40 | 55, 41.5: 63 | 58
+//   tiles, of 16 items:
+//     4 rows of 128: 32: 19 | 26, 64: 26 | 28, 96: 31 | 32, 128: 37 | 36, 192: 49 | 44
+//     one row of 64: 64: 19 | 24, 128: 27 | 29, 192: 35 | 33
+//     20 rows of 64: 64: 20 | 41, 128: 29 | 50, 192: 37 | 56
+//   all for sequences of one length: where they differ, a cluster's share grows with
+//   its own sequence, a dealt CTA's with all, so the border is below where these meet.
+//   Places that are not filled count as tiles (lengths are not known here): in a table
+//   of 32768, 16 heads of 64 against 300 tokens take 19.5 us dealt, in clusters 12; 20
+//   rows of each of 16 items 49, in clusters 12.
 // - Else 16 rows or fewer are bound by reading the keys (cache_rows_kernel: 16 rows
 //   of 64 heads, 819200 tokens, 294 us; the tile kernel 467), more by the products
 //   (32 rows: the tile kernel 467, blocks of 32 rows 1276).

@@ -9,7 +9,11 @@
 // fp16), every weight is <= 1 whatever the pages' scales, and no page is
 // dequantised.  m, the sums and O are fp32; the weights, times 2^14, are
 // rounded to fp16 (2^-11 relative; below 2^-28 of the row's largest weight, an
-// absolute 2^-39 of it).
+// absolute 2^-39 of it), because the products take 16-bit numbers: a second part of
+// each weight would be half as many products again, for an eighth of what the
+// output's own rounding to bf16 may be off by.  Against 64 bits outputs are off by
+// 1.6e-3 of their norm, as ones computed in 32 bits are.  The sum that they are
+// divided by takes the weights before they are rounded.
 // Queries are held as fp16 of q 2^-e, 2^e the power of two at the row's
 // largest magnitude: exact for bf16 numbers down to 2^-17 of it, and off by
 // 2^-25 of it below.
@@ -34,9 +38,11 @@
 // memory read free of bank conflicts (key_of below).
 //
 // Measured: one token of eight sequences of 73728 to 131072 tokens, 32 query heads
-// on 8 of 128: 278 us, 6.0 TB/s (92 % of the measured copy), and 5 us of merge; 5
-// tokens of 4 sequences of 5120 to 8191, 16 heads on 4 of 64: 15.2 us, bound by the
-// 0.9 us that a warp takes for its 32 keys of a tile.
+// on 8 of 128: 270 us, 6.2 TB/s (95 % of the measured copy), and 5 us of merge; as a
+// call among others 297 us.  5 tokens of 4 sequences of 5120 to 8191, 16 heads on 4
+// of 64: 15.0 us, bound by the 0.9 us that a warp takes for its 32 keys of a tile.
+// 168 registers, what two CTAs an SM leave; of the four variants the dealt one for
+// d = 128 spills (88 bytes written, 68 read a thread).
 #pragma once
 
 #include "cache_sched.cuh"

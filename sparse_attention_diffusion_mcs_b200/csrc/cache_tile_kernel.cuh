@@ -14,8 +14,11 @@
 // Two 8-bit products (hi, then lo) cost what one 16-bit product costs, and no
 // key is converted.
 // P.V runs in fp16: the weights need more than e4m3's 4 bits, and a weight
-// whose 8-bit parts underflow would lose the tail of a long row.  Four warps
-// turn each 128-key tile of V into fp16 once (exact) for all 256 query rows.
+// whose 8-bit parts underflow would lose the tail of a long row.  A second fp16
+// part would double these products, for an eighth of what the output's own rounding
+// to bf16 may be off by: outputs are off by 1.7e-3 of their norm against 64 bits, as
+// ones computed in 32 bits are.  Four warps turn each 128-key tile of V into fp16
+// once (exact) for all 256 query rows.
 // Weights are 2^(y - m + 6) with m at most 2^8 behind the row's maximum: at
 // most 2^14, rounded to fp16 by 2^-11 relative, normal down to 2^-20 of the
 // reference's.  Sums, m and O are fp32.
@@ -34,8 +37,11 @@
 // TMEM: S0, S1 (128 columns each), O0, O1 (D columns each).  Every wait is
 // bounded.
 //
-// Measured (4680 causal rows against 32760 tokens, 24 heads of 128): 1.72 ms,
-// 1.02 PFLOP/s; the same without the conversion of V 1.63, without
+// Measured (4680 causal rows against 32760 tokens, 24 heads of 128): 1.69 to 1.87
+// ms with the clock that the power leaves, 1.04 to 0.94 PFLOP/s; 1560 rows against
+// 10920 tokens 280 us and 12 of merge.  ptxas spills 416 bytes written and 316 read a
+// thread, at 128 registers for all roles before the handover below.  What follows
+// was measured at 1.72 ms: without the conversion of V 1.63, without
 // exponentials 1.47 ms.  Per tile a half's softmax takes 2600 cycles beside the
 // other half's (1024 of them exponentials), and the products 2340 instead of
 // 2048: they, the conversion and the loads ask for 2330 cycles of the shared

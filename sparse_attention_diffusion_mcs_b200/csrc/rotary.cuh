@@ -17,9 +17,11 @@
 // The kernel is bound by memory: every number is read and written once.  A
 // thread owns 16 numbers of one token (8 pairs, two 16-byte vectors for 16-bit
 // types) and walks over the heads, so the angles are computed once for all
-// heads of its group.  Measured: 24 heads, 32760 tokens of 128, bf16, 3 axes, from
-// the projection's layout: 62 us, 6.5 TB/s (99 % of the measured copy); 2 x 16
-// heads, 8191 tokens of 64, 48 turned: 15.5 us, 4.3 TB/s.
+// heads of its group.  Measured, 24 heads, 32760 tokens of 128, 3 axes, from the
+// projection's layout: bf16 and fp16 70 us in a row of calls, 5.7 TB/s (88 % of the
+// measured copy), fp32 143 us, 5.6 TB/s; one bf16 call after a flush 62 us, a
+// quarter of its writes still in the cache.  2 x 16 heads, 8191 tokens of 64, 48
+// turned: 16 us, 4.2 TB/s.
 #pragma once
 
 #include <cuda_fp16.h>
