@@ -402,9 +402,10 @@ mcs_status mcs_rotate(const void *x, int dtype, int B, int H, int N, int d, cons
  * by the caller.  Token j of sequence b lies in page page_table[b, j / page],
  * slot j % page.  A stored number stands for e4m3 * scale of its page and head.
  * append writes scales that are powers of two from 2^-60 to 2^60; others may be
- * a caller's: of keys 0 to 2^60, of values 2^-60 to 2^60, or 0.  Attention
- * leaves a page with another scale out, for its head, and records
- * MCS_ERR_BAD_META.  Table entries behind a
+ * a caller's: of keys 0 to 2^90, of values 2^-90 to 2^90, or 0, of one sequence
+ * and head at most 2^120 apart (0 counts as 2^-91; further, the weights of the
+ * smaller ones may be lost).  Attention leaves a page with another scale out, for
+ * its head, and records MCS_ERR_BAD_META.  Table entries behind a
  * sequence's last page are never read.  An entry outside [0, n_pages) that is
  * needed records MCS_ERR_BAD_META in the status word and is never followed:
  * append writes nothing there, read gives zeros, attention leaves the page's

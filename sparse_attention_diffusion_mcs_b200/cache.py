@@ -28,7 +28,7 @@ class KVCache(_Handle):
     k_scale, v_scale float32 [n_pages, H], page_table int32 [B, max_pages].
     Token j of sequence b is slot j % page of page page_table[b, j // page].
     A number stands for e4m3 * scale of its page and head.  Scales of a caller's own
-    are 0 to 2^60 for keys, 2^-60 to 2^60, or 0, for values; attention leaves out,
+    are 0 to 2^90 for keys, 2^-90 to 2^90, or 0, for values; attention leaves out,
     and records (last_device_status), a page whose scale is none of these.
 
     Calls work on these very buffers: change their contents in place (new pages

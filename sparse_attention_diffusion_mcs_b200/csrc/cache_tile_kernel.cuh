@@ -632,9 +632,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1) cache_tile_kernel(cons
           tc_fence_before();
           warp_arrive(b_p(half));
         }
-        // sums of products stay below 2^24 and scales are at most 2^60: from 2^40 on scores
+        // sums of products stay below 2^24 and scales are at most 2^90: from 2^13 on scores
         // may leave fp32.  Above it they make NaN; a row with keys and all its scores below is NaN too.
-        if (rowf >= 0x1p40f && m_run == -INFINITY && lim > (sg.t0 + skip) * BN) l_run = NAN;
+        if (rowf >= 0x1p13f && m_run == -INFINITY && lim > (sg.t0 + skip) * BN) l_run = NAN;
         if (ok && !mbar_wait_warp(b_o(half), n_part & 1, a.wait_ns, abort_flag)) ok = false;
         ++n_part;
         if (!ok) break;

@@ -37,16 +37,18 @@ struct CacheView {
   int n_pages, max_pages, H, page, d;
 };
 
-// Scales that attention takes: of keys 0 to 2^60, of values 2^-60 to 2^60, or 0 (the
+// Scales that attention takes: of keys 0 to 2^90, of values 2^-90 to 2^90, or 0 (the
 // values are 0, whatever the bytes).  Others are recorded and the page is left out.
+// (Weights of 2^14 over a scale of 2^-91 sum up to less than 2^127 for 2^22 tokens;
+// weights are flushed 2^140 below their row's reference, which goes by 2^x vs.)
 __device__ __forceinline__ bool scales_fit(float ks, float vs) {
-  return ks >= 0.f && ks <= 0x1p60f && (vs == 0.f || (vs >= 0x1p-60f && vs <= 0x1p60f));
+  return ks >= 0.f && ks <= 0x1p90f && (vs == 0.f || (vs >= 0x1p-90f && vs <= 0x1p90f));
 }
 // What attention reads of a page: (ks, log2 vs, 1 / vs, w); log2 vs is -inf where
-// there is none, and -61 for a vs of 0: below kHasValues the bytes of V count as 0.
-constexpr float kHasValues = -60.5f;
+// there is none, and -91 for a vs of 0: below kHasValues the bytes of V count as 0.
+constexpr float kHasValues = -90.5f;
 __device__ __forceinline__ float4 page_factors(bool have, float ks, float vs, float w) {
-  const float v = vs == 0.f ? 0x1p-61f : vs;
+  const float v = vs == 0.f ? 0x1p-91f : vs;
   return make_float4(ks, have ? __log2f(v) : -INFINITY, have ? 1.f / v : 0.f, w);
 }
 

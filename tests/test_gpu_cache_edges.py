@@ -186,7 +186,7 @@ def test_scales_of_a_callers_own(Nq, d, page, places):
 
 @pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
 @pytest.mark.parametrize("Nq", [1, 40])
-@pytest.mark.parametrize("bad", [math.nan, math.inf, -1.0, 2.0 ** 61, 2.0 ** -61])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -1.0, 2.0 ** 91, 2.0 ** -91])
 def test_scales_out_of_range_are_recorded(bad, Nq, places):
     """A page with such a scale is left out of its head's attention, and recorded, as a bad page is."""
     cache = random_cache(1, 2, [300], 64, 32, seed=8, spread=0.0, places=places)
@@ -206,3 +206,23 @@ def test_scales_out_of_range_are_recorded(bad, Nq, places):
         assert_within(O[:, 0], ref[:, 0], bound(Q, cache, [300], A, E)[:, 0])
         assert_within(O[:, 1], other[:, 1], bound(Q, cache, [300], A1, E1)[:, 1])
     assert mcs.last_device_status() == 0
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("Nq", [1, 40])
+@pytest.mark.parametrize("v,k", [(-90, -6), (-75, -6), (90, -6), (-6, 90), (-6, -100)])
+def test_scales_at_their_ends(v, k, Nq, places):
+    """All of a head's scales far out, one page 2^20 apart: as exact as others (keys:
+    the softmax's scale brings the scores back)."""
+    cache = random_cache(1, 2, [300], 64, 32, seed=8, spread=0.0, places=places)
+    table = cache.page_table[0].tolist()
+    cache.v_scale.fill_(2.0 ** v)
+    cache.v_scale[table[1]] = 2.0 ** (v - 20 if v > 0 else v + 20)
+    cache.k_scale.fill_(2.0 ** k)
+    scale = 2.0 ** (-9 - k)
+    g = torch.Generator().manual_seed(12)
+    Q = torch.randn((1, 2, Nq, 64), generator=g).to(torch.bfloat16)
+    ref, lse, A, E = attended(Q, cache, [300], False, scale=scale)
+    O, got = mcs.cache_attention(Q.cuda(), cache, i32(300), scale=scale, return_lse=True)
+    assert_within(O, ref, bound(Q, cache, [300], A, E, scale))
+    assert ((got.cpu().to(F64) - lse).abs() <= score_error(Q, cache, E, scale) + 2e-5 + 1e-6 * lse.abs()).all()
