@@ -238,8 +238,10 @@ constexpr int kRotateThreads = 256;
 // any strides, alignment and number of pairs.  Numbers that stay keep their bits.
 // MIXED: some unit has pairs of both kinds (interleaved, pairs no multiple of 8); a
 // kernel of its own, whose kept vectors would cost the other a CTA of three on an SM.
+// CTAs an SM: 8 without vectors (at 40 registers instead of 32 a head of 64 with 22
+// turned took 165 us for 134), 3 with them, 2 MIXED.
 template <typename T, bool VEC, bool MIXED>
-__global__ void __launch_bounds__(kRotateThreads, VEC && !MIXED ? 3 : 1)
+__global__ void __launch_bounds__(kRotateThreads, VEC ? (MIXED ? 2 : 3) : 8)
     rotate_kernel(const __grid_constant__ RotateArgs a) {
   const int per_token = VEC ? a.d / 16 : a.d - a.t.pairs;   // units, or pairs and single numbers behind them
   const long long id = static_cast<long long>(blockIdx.x) * kRotateThreads + threadIdx.x;
