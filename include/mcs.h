@@ -465,8 +465,8 @@ mcs_status mcs_cache_read(const mcs_cache *cache, const int32_t *start, const in
  *   sees the places up to its own; else every query sees all.
  * lse: float32 [B, Hq, Nq] or NULL: log of the sum of exp of a row's scores.
  * A row that sees nothing gives zeros, and -inf in lse; a query that is not
- * finite gives NaN, and so does a row whose largest score lies beyond fp32's
- * range (in units of log 2).  Weights and products:
+ * finite gives NaN, and so does a row all of whose scores lie beyond fp32's range
+ * (in units of log 2), and so may a row with some.  Weights and products:
  * fp32 sums and statistics of exact 8-bit numbers and 16-bit weights.
  * workspace: 16-byte aligned device memory of the size that the first function
  *   gives for the same cache, Hq and Nq (0: none needed), this call's own until

@@ -172,7 +172,7 @@ def cache_attention(Q: torch.Tensor, cache: KVCache, lengths: torch.Tensor, caus
     and sees the places up to its own.  counts (int32 [B], default Nq): query
     tokens of each sequence; rows behind give zeros, as rows do that see
     nothing (lse -inf).  A query that is not finite gives NaN, and so does a row
-    whose largest score lies beyond fp32's range.  `out` must not
+    all of whose scores lie beyond fp32's range.  `out` must not
     overlap Q.  For inference: no gradient flows through the cache."""
     _check_cache(cache)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 4:

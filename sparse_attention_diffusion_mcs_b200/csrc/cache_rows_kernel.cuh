@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 2)
     for (int u = 0; u < 2; ++u) {
       // sums of products stay below 2^17 and scales are at most 2^90: from 2^20 on scores
       // may leave fp32.  Above it they make NaN; a row with keys and all its scores below is NaN too.
-      const bool lost = rowf[u] >= 0x1p20f && m[u] == -INFINITY && lim[u] > sg.t0 * BN + warp * 32;
+      const bool lost = rowf[u] >= 0x1p20f && m[u] == -INFINITY && sg.t0 < sg.t1 && lim[u] > sg.t0 * BN + warp * 32;
       float s = lost ? NAN : l[u];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);

@@ -107,13 +107,13 @@ def test_values_that_cancel(Nq, n, d, places):
     assert_within(O, ref, bound(Q, cache, [n], A, E))
 
 
-@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("places", [0, 4096, WIDE], ids=["clusters", "idle", "dealt"])
 @pytest.mark.parametrize("Nq", [1, 40])
 @pytest.mark.parametrize("power", [-90, -60, 90, 105, 120, 127])
 def test_queries_of_any_finite_size(power, Nq, places):
     """Small keys bring the scores back to an ordinary size (scales of 2^-60, and
     the softmax's scale for the rest): rows of huge and tiny numbers are as
-    exact as others."""
+    exact as others, where some CTAs of a cluster have no tile (idle) too."""
     d, n = 64, 200
     cache = random_cache(1, 2, [n], d, 32, seed=4, spread=0.0, places=places)
     down = min(max(-power, -60), 60)
@@ -133,7 +133,7 @@ def test_queries_of_any_finite_size(power, Nq, places):
     assert ((got.cpu().to(F64) - lse).abs() <= score_error(Q, cache, E, scale) + 1e-5 + 1e-6 * lse.abs()).all()
 
 
-@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("places", [0, 4096, WIDE], ids=["clusters", "idle", "dealt"])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("Nq", [1, 40])
 def test_scores_beyond_fp32_give_nan(Nq, sign, places):
@@ -226,3 +226,38 @@ def test_scales_at_their_ends(v, k, Nq, places):
     O, got = mcs.cache_attention(Q.cuda(), cache, i32(300), scale=scale, return_lse=True)
     assert_within(O, ref, bound(Q, cache, [300], A, E, scale))
     assert ((got.cpu().to(F64) - lse).abs() <= score_error(Q, cache, E, scale) + 2e-5 + 1e-6 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("places", [0, WIDE], ids=["clusters", "dealt"])
+@pytest.mark.parametrize("Nq", [1, 40, 300])
+def test_far_apart_scales_are_as_exact(Nq, places):
+    """Value scales 2^-26 to 2^14 over the pages, queries 2^-40 to 2^4: `bound` holds here
+    too, for a row's largest term is at most the largest value, whichever page it lies in."""
+    cache = random_cache(1, 2, [777], 64, 16, seed=5, spread=12.0, places=places)
+    cache.k_scale.fill_(2.0 ** -7)
+    g = torch.Generator().manual_seed(19)
+    Q = torch.randn((1, 2, Nq, 64), generator=g) * torch.exp2(torch.randint(-40, 4, (1, 2, Nq, 1), generator=g).float())
+    Q = Q.to(torch.bfloat16)
+    ref, lse, A, E = attended(Q, cache, [777], False, scale=0.7)
+    O, got = mcs.cache_attention(Q.cuda(), cache, i32(777), scale=0.7, return_lse=True)
+    assert_within(O, ref, bound(Q, cache, [777], A, E, 0.7))
+    assert ((got.cpu().to(F64) - lse).abs() <= score_error(Q, cache, E, 0.7) + 1e-5 + 1e-6 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("places", [64, WIDE], ids=["clusters", "dealt"])
+def test_append_onto_a_page_of_zero_scales(places):
+    """Tokens held at scales of 0 stand for zeros; a new token gives the page scales, and
+    they stay zeros beside it."""
+    cache = mcs.KVCache.empty(1, 1, places, 64, 16)
+    g = torch.Generator().manual_seed(2)
+    K, V = (torch.randn((1, 1, 9, 64), generator=g).to(torch.bfloat16) for _ in range(2))
+    mcs.cache_append(cache, K[:, :, :5].cuda(), V[:, :, :5].cuda(), i32(0))
+    cache.k_scale.zero_()
+    cache.v_scale.zero_()
+    mcs.cache_append(cache, K[:, :, 5:].cuda(), V[:, :, 5:].cuda(), i32(5))
+    k, v = mcs.cache_read(cache, i32(0), 9)
+    assert (k[:, :, :5] == 0).all() and (v[:, :, :5] == 0).all()
+    assert ((k[:, :, 5:].cpu().float() - K[:, :, 5:].float()).abs() <= K[:, :, 5:].float().abs() / 16 + 2.0 ** -15).all()
+    Q = torch.randn((1, 2, 3, 64), generator=g).to(torch.bfloat16)
+    ref, _, A, E = attended(Q, cache, [9], True)
+    assert_within(mcs.cache_attention(Q.cuda(), cache, i32(9), causal=True), ref, bound(Q, cache, [9], A, E))
