@@ -111,7 +111,7 @@ def cache_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, start: torch.
     all), where the sequence then ends.
 
     rotary: keys are turned on the way, by `positions` (as in `rotate`) or by
-    their places."""
+    their places.  No gradient flows into the cache."""
     _check_cache(cache)
     for t, name in ((K, "K"), (V, "V")):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != cache.device or t.dim() != 4:

@@ -39,7 +39,7 @@
 //
 // Measured: one token of eight sequences of 73728 to 131072 tokens, 32 query heads
 // on 8 of 128: 270 us, 6.2 TB/s (95 % of the measured copy), and 5 us of merge; as a
-// call among others 297 us.  5 tokens of 4 sequences of 5120 to 8191, 16 heads on 4
+// call among others 297 to 315 us.  5 tokens of 4 sequences of 5120 to 8191, 16 heads on 4
 // of 64: 15.0 us, bound by the 0.9 us that a warp takes for its 32 keys of a tile.
 // 168 registers, what two CTAs an SM leave; of the four variants the dealt one for
 // d = 128 spills (88 bytes written, 68 read a thread).
